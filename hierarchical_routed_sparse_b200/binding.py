@@ -19,6 +19,7 @@ import torch
 HGA_OK, HGA_ERR_INVALID_ARG, HGA_ERR_UNSUPPORTED, HGA_ERR_CUDA, HGA_ERR_DEVICE_CHECK = 0, 1, 2, 3, 4
 HGA_ALL = -1
 HGA_BF16, HGA_FP32 = 0, 1
+HGA_INT8, HGA_E4M3 = 2, 3            # held values of a paged cache
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libhga.so")
 # The bounds-checked build of the same library (-DHGA_CHECK_BOUNDS).
@@ -29,7 +30,8 @@ EXPORTS = ("hga_route_widths", "hga_workspace_size", "hga_build_summaries", "hga
            "hga_route_groups", "hga_route", "hga_attn_fwd", "hga_route_attn_fwd", "hga_attn_bwd", "hga_attn_bwd_noalloc",
            "hga_stage_params", "hga_stage_routed", "hga_decode", "hga_route_causal", "hga_causal_sched_size",
            "hga_causal_schedule", "hga_attn_fwd_causal", "hga_attn_bwd_causal", "hga_device_status", "hga_device_check", "hga_checked_build",
-           "hga_selftest_wait", "hga_last_error",
+           "hga_rope_fwd", "hga_rope_bwd", "hga_paged_widths", "hga_paged_workspace_size", "hga_paged_append",
+           "hga_paged_decode", "hga_selftest_wait", "hga_last_error",
            "hga_version")
 NOALLOC_MAX_ROWS = 1 << 20     # HGA_NOALLOC_MAX_ROWS
 
@@ -46,6 +48,23 @@ class _Params(ctypes.Structure):
                 ("chunk", ctypes.c_int), ("group", ctypes.c_int), ("qblock", ctypes.c_int),
                 ("k_c", ctypes.c_int), ("k_g", ctypes.c_int), ("scale", ctypes.c_float),
                 ("dtype", ctypes.c_int), ("kv_capacity", ctypes.c_int64)]
+
+
+class _RopeParams(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int) for n in ("B", "H", "d", "rot_dim", "interleaved", "x_dtype", "y_dtype")] +
+                [(n, ctypes.c_int64) for n in ("T", "pos0", "table_rows", "x_batch", "x_token", "x_head")])
+
+
+class _PagedParams(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("d", ctypes.c_int),
+                ("max_chunks", ctypes.c_int), ("n_pages", ctypes.c_int64), ("k_c", ctypes.c_int),
+                ("k_g", ctypes.c_int), ("scale", ctypes.c_float), ("dtype", ctypes.c_int),
+                ("cache_dtype", ctypes.c_int)]
+
+
+class _PagedCache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k_pages", "v_pages", "k_scale", "v_scale", "csum", "gsum", "k_tail",
+                                               "v_tail", "table")]
 
 
 @dataclass
@@ -130,6 +149,15 @@ def load() -> ctypes.CDLL:
             "hga_causal_schedule": ([PP, P, P, P], ctypes.c_int),
             "hga_attn_fwd_causal": ([PP, P, P, P, P, P, P, P, P], ctypes.c_int),
             "hga_attn_bwd_causal": ([PP, P, P, P, P, P, P, P, P, P, P, P, P], ctypes.c_int),
+            "hga_rope_fwd": ([ctypes.POINTER(_RopeParams), P, P, P, P], ctypes.c_int),
+            "hga_rope_bwd": ([ctypes.POINTER(_RopeParams), P, P, P, P], ctypes.c_int),
+            "hga_paged_widths": ([ctypes.POINTER(_PagedParams), ctypes.POINTER(ctypes.c_int),
+                                  ctypes.POINTER(ctypes.c_int)], ctypes.c_int),
+            "hga_paged_workspace_size": ([ctypes.POINTER(_PagedParams)], ctypes.c_size_t),
+            "hga_paged_append": ([ctypes.POINTER(_PagedParams), ctypes.POINTER(_PagedCache), P, P, I64, P, I64, I64,
+                                  P, I64, I64, P, I64, I64, P, P, I64, ctypes.c_int, ctypes.c_int, P], ctypes.c_int),
+            "hga_paged_decode": ([ctypes.POINTER(_PagedParams), ctypes.POINTER(_PagedCache), P, P, P, P, P, P, P,
+                                  ctypes.c_size_t, P], ctypes.c_int),
             "hga_device_status": ([ctypes.POINTER(ctypes.c_int), ctypes.c_int], ctypes.c_int),
             "hga_selftest_wait": ([ctypes.c_int, ctypes.POINTER(ctypes.c_int), P], ctypes.c_int),
             "hga_device_check": ([ctypes.POINTER(ctypes.c_int), ctypes.c_int], ctypes.c_int),
@@ -337,6 +365,69 @@ def attn_bwd_causal(p: Params, Q, K, V, O, lse, dO, gidx, dQ, dK_seg, dV_seg, st
     _check(load().hga_attn_bwd_causal(ctypes.byref(p.c()), _ptr(Q), _ptr(K), _ptr(V), _ptr(O), _ptr(lse),
                                       _ptr(dO), _ptr(gidx), _ptr(sched), _ptr(dQ), _ptr(dK_seg), _ptr(dV_seg),
                                       _stream(stream)))
+
+
+_HGA_DTYPE = {torch.bfloat16: HGA_BF16, torch.float32: HGA_FP32}
+
+
+def _here(t: torch.Tensor, name: str) -> int:
+    """Data pointer of a tensor on the current device (kernels run there)."""
+    if not t.is_cuda:
+        raise ValueError("libhga takes device tensors")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on device {t.get_device()}, the current device is {torch.cuda.current_device()}")
+    return t.data_ptr()
+
+
+def _hga_dtype(t: torch.Tensor, name: str) -> int:
+    code = _HGA_DTYPE.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bfloat16 or float32 (got {t.dtype})")
+    return code
+
+
+def rope_table(rows: int, rot_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """Cosines, then sines, of positions 0 .. rows - 1 (float32 [rows][rot_dim])
+    at the angles pos * base^(-2i / rot_dim), formed in float64."""
+    if rows < 1 or rot_dim < 16 or rot_dim % 16:
+        raise ValueError(f"need rows >= 1 and rot_dim a positive multiple of 16 (got {rows}, {rot_dim})")
+    f = base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    a = torch.arange(rows, dtype=torch.float64, device=device)[:, None] * f
+    return torch.cat([a.cos(), a.sin()], 1).float()
+
+
+def _check_table(table, name: str) -> None:
+    if table.dtype != torch.float32 or table.dim() != 2 or not table.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous float32 [rows][rot_dim] tensor")
+
+
+def _rope(call, src, dst, x, y, table, pos0: int, interleaved: bool, stream) -> None:
+    if x.dim() != 4 or y.dim() != 4 or x.stride(3) != 1 or not y.is_contiguous():
+        raise ValueError("rope takes [B][T][H][d] rows with unit stride along d and a contiguous [B][H][T][d]")
+    B_, T, H, d = x.shape
+    if tuple(y.shape) != (B_, H, T, d):
+        raise ValueError(f"shapes {tuple(x.shape)} and {tuple(y.shape)} are not [B][T][H][d] and [B][H][T][d]")
+    rot = rows = 0
+    if table is not None:
+        _check_table(table, "table")
+        rows, rot = table.shape
+    xs = x.stride()
+    p = _RopeParams(B_, H, d, rot, int(interleaved), _hga_dtype(x, "x"), _hga_dtype(y, "y"), T, pos0, rows, xs[0],
+                    xs[1], xs[2])
+    _check(call(ctypes.byref(p), _here(src, "the input"), None if table is None else _here(table, "table"),
+                _here(dst, "the output"), _stream(stream)))
+
+
+def rope_fwd(x, y, table, pos0: int = 0, interleaved: bool = False, stream=None) -> None:
+    """y [B][H][T][d] = x [B][T][H][d] (any strides with unit stride along d)
+    rotated by positions pos0 + t; ``table`` as of ``rope_table`` (None: no
+    rotation, only the layout and the type change)."""
+    _rope(load().hga_rope_fwd, x, y, x, y, table, pos0, interleaved, stream)
+
+
+def rope_bwd(dy, dx, table, pos0: int = 0, interleaved: bool = False, stream=None) -> None:
+    """Gradient of ``rope_fwd``: dx [B][T][H][d] (strided) from dy [B][H][T][d]."""
+    _rope(load().hga_rope_bwd, dy, dx, dx, dy, table, pos0, interleaved, stream)
 
 
 class CausalBuffers:

@@ -55,7 +55,8 @@ int read_check_words(bool clear)
 {
     int (*const readers[])(bool) = {hga::check_word_attn_tc_fwd, hga::check_word_attn_tc_bwd,
                                     hga::check_word_attn_simt,   hga::check_word_causal,
-                                    hga::check_word_router,      hga::check_word_stage};
+                                    hga::check_word_router,      hga::check_word_stage,
+                                    hga::check_word_paged_append, hga::check_word_paged_decode};
     int first = 0;
     for (auto f : readers) {
         const int v = f(clear);
@@ -79,8 +80,8 @@ int finish(cudaError_t e, cudaStream_t st, const char* name)
     if (w < 0) return fail(HGA_ERR_CUDA, "%s: the bounds-check word could not be read", name);
     if (w)
         return fail(HGA_ERR_DEVICE_CHECK,
-                    "%s: device bounds check %d failed: an index row holds an entry outside its valid range "
-                    "(outputs are invalid)", name, w);
+                    "%s: device bounds check %d failed: an index row, page table, position or token offset holds an "
+                    "entry outside its valid range (outputs are invalid)", name, w);
 #else
     (void)st;
 #endif
@@ -515,6 +516,213 @@ int hga_attn_bwd_causal(const hga_params* p, const void* Q, const void* K, const
     cudaError_t e = hga::launch_attn_bwd_causal(s, Q, K, V, O, lse, dO, gidx, sched, dQ, dK_seg, dV_seg,
                                                 static_cast<cudaStream_t>(stream));
     return finish(e, static_cast<cudaStream_t>(stream), "hga_attn_bwd_causal");
+}
+
+// ---- position rotation ----------------------------------------------------------
+
+// Rows of `el`-byte elements by strides: non-negative multiples of 16 bytes.
+static int check_stride(int64_t stride, int el, const char* name)
+{
+    if (stride < 0 || stride % (16 / el))
+        return fail(HGA_ERR_INVALID_ARG, "%s (%lld) must be non-negative and span a multiple of 16 bytes", name,
+                    (long long)stride);
+    return HGA_OK;
+}
+
+static int element_bytes(int dtype) { return dtype == HGA_BF16 ? 2 : 4; }
+
+static int check_rotation(int rot_dim, int d, const float* table, const char* name)
+{
+    if (rot_dim < 0 || rot_dim > d || rot_dim % 16)
+        return fail(HGA_ERR_INVALID_ARG, "rot_dim (%d) must be a multiple of 16 in [0, d=%d]", rot_dim, d);
+    if (rot_dim > 0) {
+        if (!table) return fail(HGA_ERR_INVALID_ARG, "%s is NULL", name);
+        if (!aligned16(table)) return fail(HGA_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
+    }
+    return HGA_OK;
+}
+
+static int run_rope(const hga_rope_params* p, bool back, const void* src, const float* table, void* dst,
+                    hga_stream_t stream, const char* name)
+{
+    if (!p) return fail(HGA_ERR_INVALID_ARG, "params is NULL");
+    if (p->B < 1 || p->H < 1) return fail(HGA_ERR_INVALID_ARG, "B, H must be >= 1 (got %d, %d)", p->B, p->H);
+    if (p->d != 64 && p->d != 128) return fail(HGA_ERR_UNSUPPORTED, "head dim d=%d (supported: 64, 128)", p->d);
+    for (int t : {p->x_dtype, p->y_dtype})
+        if (t != HGA_BF16 && t != HGA_FP32)
+            return fail(HGA_ERR_INVALID_ARG, "dtype %d is neither HGA_BF16 nor HGA_FP32", t);
+    if (p->T < 0 || p->pos0 < 0 || p->T > INT32_MAX || p->pos0 > INT32_MAX)
+        return fail(HGA_ERR_INVALID_ARG, "T (%lld) and pos0 (%lld) must lie in [0, 2^31)", (long long)p->T,
+                    (long long)p->pos0);
+    if (int r = check_rotation(p->rot_dim, p->d, table, "table")) return r;
+    if (p->rot_dim > 0 && p->pos0 + p->T > p->table_rows)
+        return fail(HGA_ERR_INVALID_ARG, "positions up to %lld exceed the table of %lld rows",
+                    (long long)(p->pos0 + p->T), (long long)p->table_rows);
+    const int el = element_bytes(p->x_dtype);
+    if (int r = check_stride(p->x_batch, el, "x_batch")) return r;
+    if (int r = check_stride(p->x_token, el, "x_token")) return r;
+    if (int r = check_stride(p->x_head, el, "x_head")) return r;
+    if (p->T == 0) return HGA_OK;
+    if (!src || !dst) return fail(HGA_ERR_INVALID_ARG, "%s: an input or output is NULL", name);
+    if (!aligned16(src) || !aligned16(dst))
+        return fail(HGA_ERR_INVALID_ARG, "%s: an input or output is not 16-byte aligned", name);
+    const hga::RopeShape s{p->B,      p->H,       p->d,       p->rot_dim, p->interleaved != 0, p->T, p->pos0,
+                           p->x_batch, p->x_token, p->x_head, p->x_dtype, p->y_dtype};
+    if (!hga::rope_grid_fits(s)) return fail(HGA_ERR_UNSUPPORTED, "problem too large for one launch grid");
+    const cudaError_t e = hga::launch_rope(s, back, src, table, dst, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? HGA_OK : cuda_fail(e, name);
+}
+
+int hga_rope_fwd(const hga_rope_params* p, const void* x, const float* table, void* y, hga_stream_t stream)
+{
+    const NvtxRange nvtx_range("hga_rope_fwd");
+    return run_rope(p, false, x, table, y, stream, "hga_rope_fwd");
+}
+
+int hga_rope_bwd(const hga_rope_params* p, const void* dy, const float* table, void* dx, hga_stream_t stream)
+{
+    const NvtxRange nvtx_range("hga_rope_bwd");
+    return run_rope(p, true, dy, table, dx, stream, "hga_rope_bwd");
+}
+
+// ---- paged cache -------------------------------------------------------------------
+
+static int paged_shape(const hga_paged_params* p, hga::PagedShape* s)
+{
+    if (!p) return fail(HGA_ERR_INVALID_ARG, "params is NULL");
+    if (p->B < 1 || p->Hq < 1 || p->Hkv < 1)
+        return fail(HGA_ERR_INVALID_ARG, "B, Hq, Hkv must be >= 1 (got %d, %d, %d)", p->B, p->Hq, p->Hkv);
+    if (p->Hq % p->Hkv != 0)
+        return fail(HGA_ERR_INVALID_ARG, "Hq (%d) must be a multiple of Hkv (%d)", p->Hq, p->Hkv);
+    if (p->d != 64 && p->d != 128) return fail(HGA_ERR_UNSUPPORTED, "head dim d=%d (supported: 64, 128)", p->d);
+    if (p->max_chunks < 1 || p->n_pages < 1 || p->n_pages > INT32_MAX)
+        return fail(HGA_ERR_INVALID_ARG, "max_chunks (%d) must be >= 1 and n_pages (%lld) in [1, 2^31)", p->max_chunks,
+                    (long long)p->n_pages);
+    if ((p->k_c < 1 && p->k_c != HGA_ALL) || (p->k_g < 1 && p->k_g != HGA_ALL))
+        return fail(HGA_ERR_INVALID_ARG, "k_c (%d) and k_g (%d) must be >= 1 or HGA_ALL", p->k_c, p->k_g);
+    if (p->dtype != HGA_BF16 && p->dtype != HGA_FP32)
+        return fail(HGA_ERR_INVALID_ARG, "dtype %d is neither HGA_BF16 nor HGA_FP32", p->dtype);
+    if (p->cache_dtype != HGA_INT8 && p->cache_dtype != HGA_E4M3)
+        return fail(HGA_ERR_INVALID_ARG, "cache_dtype %d is neither HGA_INT8 nor HGA_E4M3", p->cache_dtype);
+    if (!std::isfinite(p->scale) || p->scale < 0.f)
+        return fail(HGA_ERR_INVALID_ARG, "scale must be finite and >= 0 (0 selects 1/sqrt(d))");
+    const int64_t wc = p->k_c == HGA_ALL ? p->max_chunks : p->k_c;
+    const int64_t wg = p->k_g == HGA_ALL ? wc * hga::kGroupsPerChunk : p->k_g;
+    if (p->max_chunks > INT32_MAX / 64 || wc > INT32_MAX / 64 || wg > INT32_MAX / 64)
+        return fail(HGA_ERR_UNSUPPORTED, "max_chunks (%d) or routing widths (%lld, %lld) too large", p->max_chunks,
+                    (long long)wc, (long long)wg);
+    if ((int64_t)p->B * p->Hkv > INT32_MAX / 64 || (int64_t)p->B * p->Hq > INT32_MAX / 64)
+        return fail(HGA_ERR_UNSUPPORTED, "problem too large for one launch grid");
+    s->B = p->B; s->Hq = p->Hq; s->Hkv = p->Hkv; s->G = p->Hq / p->Hkv; s->d = p->d;
+    s->n_pages = p->n_pages; s->max_chunks = p->max_chunks;
+    s->k_c = p->k_c == HGA_ALL ? 0 : p->k_c;
+    s->k_g = p->k_g == HGA_ALL ? 0 : p->k_g;
+    s->wc = (int)wc; s->wg = (int)wg;
+    s->scale = p->scale == 0.f ? 1.0f / std::sqrt((float)p->d) : p->scale;
+    s->dtype = p->dtype; s->cache_dtype = p->cache_dtype;
+    return HGA_OK;
+}
+
+static int check_cache(const hga_paged_cache* cache)
+{
+    if (!cache) return fail(HGA_ERR_INVALID_ARG, "cache is NULL");
+    CHECK_PTR(cache->k_pages);
+    CHECK_PTR(cache->v_pages);
+    CHECK_PTR(cache->k_scale);
+    CHECK_PTR(cache->v_scale);
+    CHECK_PTR(cache->csum);
+    CHECK_PTR(cache->gsum);
+    CHECK_PTR(cache->k_tail);
+    CHECK_PTR(cache->v_tail);
+    CHECK_PTR(cache->table);
+    return HGA_OK;
+}
+
+int hga_paged_widths(const hga_paged_params* p, int* wc, int* wg)
+{
+    hga::PagedShape s{};
+    if (int r = paged_shape(p, &s)) return r;
+    if (!wc || !wg) return fail(HGA_ERR_INVALID_ARG, "wc / wg output pointer is NULL");
+    *wc = s.wc;
+    *wg = s.wg;
+    return HGA_OK;
+}
+
+size_t hga_paged_workspace_size(const hga_paged_params* p)
+{
+    hga::PagedShape s{};
+    if (paged_shape(p, &s)) return 0;
+    return hga::paged_workspace(s);
+}
+
+int hga_paged_append(const hga_paged_params* p, const hga_paged_cache* c, const int32_t* pos,
+                     const int32_t* cu_tokens, int64_t N, const void* q, int64_t q_token, int64_t q_head,
+                     const void* k, int64_t k_token, int64_t k_head, const void* v, int64_t v_token,
+                     int64_t v_head, void* q_out, const float* rope, int64_t rope_rows, int rot_dim,
+                     int interleaved, hga_stream_t stream)
+{
+    const NvtxRange nvtx_range("hga_paged_append");
+    hga::PagedShape s{};
+    if (int r = paged_shape(p, &s)) return r;
+    if (N < 0 || N > INT32_MAX) return fail(HGA_ERR_INVALID_ARG, "N (%lld) must lie in [0, 2^31)", (long long)N);
+    if (!cu_tokens && N != s.B)
+        return fail(HGA_ERR_INVALID_ARG, "without cu_tokens N (%lld) must be B (%d): one token each", (long long)N, s.B);
+    if (int r = check_rotation(rot_dim, s.d, rope, "rope")) return r;
+    if (rot_dim > 0 && rope_rows < 1) return fail(HGA_ERR_INVALID_ARG, "rope_rows (%lld) must be >= 1", (long long)rope_rows);
+    const int el = element_bytes(s.dtype);
+    if (int r = check_stride(k_token, el, "k_token")) return r;
+    if (int r = check_stride(k_head, el, "k_head")) return r;
+    if (int r = check_stride(v_token, el, "v_token")) return r;
+    if (int r = check_stride(v_head, el, "v_head")) return r;
+    if (q) {
+        if (int r = check_stride(q_token, el, "q_token")) return r;
+        if (int r = check_stride(q_head, el, "q_head")) return r;
+    }
+    if (!q != !q_out) return fail(HGA_ERR_INVALID_ARG, "q and q_out go together");
+    if (N == 0) return HGA_OK;
+    if (int r = check_cache(c)) return r;
+    if (!pos) return fail(HGA_ERR_INVALID_ARG, "pos is NULL");
+    CHECK_PTR(k);
+    CHECK_PTR(v);
+    if (q) {
+        CHECK_PTR(q);
+        CHECK_PTR(q_out);
+    }
+    const hga::PagedAppend a{pos,   cu_tokens, N,    {q, q_token, q_head}, {k, k_token, k_head}, {v, v_token, v_head},
+                             q_out, rope,      rope_rows, rot_dim,          interleaved != 0};
+    if (!hga::paged_append_grid_fits(s, a)) return fail(HGA_ERR_UNSUPPORTED, "problem too large for one launch grid");
+    const auto st = static_cast<cudaStream_t>(stream);
+    return finish(hga::launch_paged_append(s, *c, a, st), st, "hga_paged_append");
+}
+
+int hga_paged_decode(const hga_paged_params* p, const hga_paged_cache* c, const int32_t* pos, const void* q,
+                     float* O, float* lse, int32_t* cidx, int32_t* gidx, void* workspace, size_t ws_bytes,
+                     hga_stream_t stream)
+{
+    const NvtxRange nvtx_range("hga_paged_decode");
+    hga::PagedShape s{};
+    if (int r = paged_shape(p, &s)) return r;
+    if (s.G > hga::decode_max_heads())
+        return fail(HGA_ERR_UNSUPPORTED, "decode takes at most %d q-heads per kv-head (got %d)",
+                    hga::decode_max_heads(), s.G);
+    if (int r = check_cache(c)) return r;
+    if (!pos) return fail(HGA_ERR_INVALID_ARG, "pos is NULL");
+    CHECK_PTR(q);
+    CHECK_PTR(O);
+    CHECK_PTR(lse);
+    if (cidx || gidx || s.k_c > 0 || s.k_g > 0) {
+        CHECK_PTR(cidx);
+        CHECK_PTR(gidx);
+        if (hga::paged_decode_smem(s) > kMaxSmem)
+            return fail(HGA_ERR_UNSUPPORTED, "routing of %d chunks / k_c=%d exceeds the kernel's shared memory",
+                        s.max_chunks, s.wc);
+    }
+    const size_t need = hga::paged_workspace(s);
+    if (need > 0) CHECK_PTR(workspace);
+    if (ws_bytes < need)
+        return fail(HGA_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu needed", ws_bytes, need);
+    const auto st = static_cast<cudaStream_t>(stream);
+    return finish(hga::launch_paged_decode(s, *c, pos, q, O, lse, cidx, gidx, workspace, st), st, "hga_paged_decode");
 }
 
 int hga_attn_fwd(const hga_params* p, const void* Q, const void* K, const void* V,

@@ -29,6 +29,43 @@ struct Shape {
     int dtype;
 };
 
+// Validated arguments of the rotation calls (rope.cu).
+struct RopeShape {
+    int B, H, d, rot;
+    bool interleaved;
+    int64_t T, pos0;
+    int64_t x_batch, x_token, x_head;   // strides of x / dx, in elements
+    int x_dtype, y_dtype;
+};
+
+// Validated shape of the paged cache's calls (paged_append.cu, paged_decode.cu).
+struct PagedShape {
+    int B, Hq, Hkv, G, d;
+    int64_t n_pages;
+    int max_chunks;          // width of the page table
+    int k_c, k_g;            // <= 0: keep all eligible
+    int wc, wg;              // index row widths
+    float scale;
+    int dtype, cache_dtype;
+};
+
+// Token rows of an append call: rows of d elements by strides (in elements).
+struct PagedRows {
+    const void* ptr;
+    int64_t token, head;
+};
+struct PagedAppend {
+    const int32_t* pos;      // [B] tokens that each sequence holds
+    const int32_t* cu;       // [B + 1] offsets into the tokens, or null: token b is sequence b's
+    int64_t N;
+    PagedRows q, k, v;       // q.ptr may be null
+    void* q_out;
+    const float* rope;       // [rope_rows][rot]
+    int64_t rope_rows;
+    int rot;
+    bool interleaved;
+};
+
 // Work items of the tensor-core backward: one per (batch, kv-head, query
 // block) and pair of q-heads.  At most B*Hq*T_seg / 64.
 inline int64_t bwd_items(const Shape& s) { return (int64_t)s.B * s.Hkv * s.nQB * ((s.G + 1) / 2); }
@@ -153,6 +190,8 @@ int check_word_attn_simt(bool clear);
 int check_word_causal(bool clear);
 int check_word_router(bool clear);
 int check_word_stage(bool clear);
+int check_word_paged_append(bool clear);
+int check_word_paged_decode(bool clear);
 int selftest_status(bool clear); // status word of selftest.cu
 int selftest_site();             // the code its wait records
 cudaError_t launch_selftest_wait(unsigned long long limit_ns, cudaStream_t st);
@@ -180,6 +219,20 @@ cudaError_t launch_attn_bwd_simt(const Shape& s, const void* Q, const void* K, c
                                  const float* O, const float* lse, const void* dO,
                                  const int32_t* gidx, float* dQ, float* dK_seg, float* dV_seg,
                                  float* Drow, cudaStream_t st);
+
+// Position rotation and its gradient (rope.cu): forward reads x by strides
+// and writes y [B][H][T][d], back the other way round.
+cudaError_t launch_rope(const RopeShape& s, bool back, const void* src, const float* table, void* dst,
+                        cudaStream_t st);
+bool rope_grid_fits(const RopeShape& s);
+// Paged cache (paged_append.cu, paged_decode.cu).
+cudaError_t launch_paged_append(const PagedShape& s, const hga_paged_cache& c, const PagedAppend& a, cudaStream_t st);
+bool paged_append_grid_fits(const PagedShape& s, const PagedAppend& a);
+cudaError_t launch_paged_decode(const PagedShape& s, const hga_paged_cache& c, const int32_t* pos, const void* q,
+                                float* O, float* lse, int32_t* cidx, int32_t* gidx, void* workspace,
+                                cudaStream_t st);
+size_t paged_decode_smem(const PagedShape& s);
+size_t paged_workspace(const PagedShape& s);
 
 // Streaming multiprocessors of the current device (cached per device).
 int sm_count();

@@ -1,0 +1,193 @@
+"""The paged 8-bit key / value cache for generation with a ragged batch.
+
+``PagedCache`` holds the cache's tensors and calls the library on them:
+``append`` puts tokens into it (rotating queries and keys on the way),
+``decode`` lets one query per sequence attend it.  Which page a chunk gets is
+the caller's choice, written into ``table``; ``PagedDecodeState`` hands pages
+out in order and generates token by token, as ``DecodeState`` does on a dense
+cache.  Positions and tables live on the device, so a captured step serves
+every position.
+"""
+from __future__ import annotations
+
+import ctypes
+from dataclasses import dataclass
+
+import torch
+
+from . import binding as B
+from .binding import HGA_ALL, HGA_BF16, HGA_E4M3, HGA_INT8
+
+_HELD = {HGA_INT8: torch.int8, HGA_E4M3: torch.float8_e4m3fn}
+
+
+@dataclass(frozen=True)
+class PagedParams:
+    """Mirror of hga_paged_params.  k_c / k_g may be HGA_ALL (-1)."""
+    B: int
+    Hq: int
+    Hkv: int
+    d: int
+    n_pages: int             # pages in the pool
+    max_chunks: int          # chunks per sequence, at most (width of the table)
+    k_c: int = HGA_ALL
+    k_g: int = HGA_ALL
+    dtype: int = HGA_BF16
+    cache_dtype: int = HGA_INT8
+    scale: float = 0.0
+
+    @property
+    def torch_dtype(self):
+        return torch.bfloat16 if self.dtype == HGA_BF16 else torch.float32
+
+    def c(self):
+        return B._PagedParams(self.B, self.Hq, self.Hkv, self.d, self.max_chunks, self.n_pages, self.k_c, self.k_g,
+                              float(self.scale), self.dtype, self.cache_dtype)
+
+
+def paged_widths(p: PagedParams) -> tuple[int, int]:
+    wc, wg = ctypes.c_int(), ctypes.c_int()
+    B._check(B.load().hga_paged_widths(ctypes.byref(p.c()), ctypes.byref(wc), ctypes.byref(wg)))
+    return wc.value, wg.value
+
+
+def paged_workspace_size(p: PagedParams) -> int:
+    """Bytes of device scratch that a decode call needs."""
+    return int(B.load().hga_paged_workspace_size(ctypes.byref(p.c())))
+
+
+def _ints(t, name, *shape):
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
+    return B._here(t, name)
+
+
+class PagedCache:
+    """The tensors of a paged cache (include/hga.h, hga_paged_cache) and the
+    scratch of its decode calls.  Tensors that are not given are allocated:
+    the pool and the open rows zeroed, the table filled with -1 (no page).
+    One cache object serves one stream at a time: its calls share the scratch
+    (the workspace that decode is given takes its place)."""
+
+    def __init__(self, p: PagedParams, device="cuda", **tensors):
+        paged_widths(p)                              # the parameters are valid
+        self.p = p
+        f32, i32 = torch.float32, torch.int32
+        held = _HELD[p.cache_dtype]
+        shapes = dict(k_pages=((p.n_pages, p.Hkv, 64, p.d), held), v_pages=((p.n_pages, p.Hkv, 64, p.d), held),
+                      k_scale=((p.n_pages, p.Hkv, 8), f32), v_scale=((p.n_pages, p.Hkv, 8), f32),
+                      csum=((p.n_pages, p.Hkv, p.d), f32), gsum=((p.n_pages, p.Hkv, 8, p.d), f32),
+                      k_tail=((p.B, p.Hkv, 64, p.d), f32), v_tail=((p.B, p.Hkv, 64, p.d), p.torch_dtype),
+                      table=((p.B, p.max_chunks), i32))
+        for name in tensors:
+            if name not in shapes:
+                raise ValueError(f"a paged cache has no tensor {name!r}")
+        ptrs = []
+        for name, (shape, dtype) in shapes.items():
+            t = tensors.get(name)
+            if t is None:
+                t = (torch.full(shape, -1, dtype=dtype, device=device) if name == "table"
+                     else torch.zeros(shape, dtype=dtype, device=device))
+            elif tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
+            setattr(self, name, t)
+            ptrs.append(B._here(t, name))
+        self._p, self._c = p.c(), B._PagedCache(*ptrs)
+        self._pp, self._pc = ctypes.byref(self._p), ctypes.byref(self._c)
+        self._widths = paged_widths(p)
+        n = paged_workspace_size(p)
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=self.table.device) if n else None
+
+    def _rows(self, t, name, N, H):
+        if tuple(t.shape) != (N, H, self.p.d) or t.dtype != self.p.torch_dtype or t.stride(2) != 1:
+            raise ValueError(f"{name} must be {self.p.torch_dtype} rows [{N}][{H}][{self.p.d}] with unit stride along d")
+        return B._here(t, name), t.stride(0), t.stride(1)
+
+    def append(self, pos, k, v, cu=None, q=None, q_out=None, rope=None, interleaved: bool = False, stream=None):
+        """Tokens cu[b] .. cu[b + 1] - 1 of k, v [N][Hkv][d] (and q [N][Hq][d])
+        join sequence b at positions pos[b], pos[b] + 1, ... (int32, device;
+        cu None: one token each).  q_out [N][Hq][d] gets the rotated queries;
+        ``rope`` as of ``rope_table`` (None: k and q are taken as they are)."""
+        p = self.p
+        N = k.shape[0]
+        kr, vr = self._rows(k, "k", N, p.Hkv), self._rows(v, "v", N, p.Hkv)
+        qr, out = (None, 0, 0), None
+        if q is not None:
+            qr = self._rows(q, "q", N, p.Hq)
+        if q_out is not None:
+            out = self._rows(q_out, "q_out", N, p.Hq)[0]
+            if not q_out.is_contiguous():
+                raise ValueError("q_out must be contiguous")
+        table, rows, rot = None, 0, 0
+        if rope is not None:
+            B._check_table(rope, "rope")
+            table = B._here(rope, "rope")
+            rows, rot = rope.shape
+        B._check(B.load().hga_paged_append(
+            self._pp, self._pc, _ints(pos, "pos", p.B), None if cu is None else _ints(cu, "cu", p.B + 1), N, *qr, *kr,
+            *vr, out, table, rows, rot, int(interleaved), B._stream(stream)))
+
+    def decode(self, pos, q, O, lse, cidx=None, gidx=None, workspace=None, stream=None):
+        """The query q [B][Hq][d] of each sequence, at position pos[b] (int32,
+        device; negative: empty), attends its cache: O [B][Hq][d] and lse
+        [B][Hq] (float32), routing rows cidx [B][Hkv][wc], gidx [B][Hkv][wg]
+        (int32; may be None when k_c = k_g = HGA_ALL)."""
+        p = self.p
+        wc, wg = self._widths
+        if tuple(q.shape) != (p.B, p.Hq, p.d) or q.dtype != p.torch_dtype or not q.is_contiguous():
+            raise ValueError(f"q must be contiguous {p.torch_dtype} [{p.B}][{p.Hq}][{p.d}]")
+        if tuple(O.shape) != (p.B, p.Hq, p.d) or O.dtype != torch.float32 or not O.is_contiguous():
+            raise ValueError(f"O must be contiguous float32 [{p.B}][{p.Hq}][{p.d}]")
+        if tuple(lse.shape) != (p.B, p.Hq) or lse.dtype != torch.float32 or not lse.is_contiguous():
+            raise ValueError(f"lse must be contiguous float32 [{p.B}][{p.Hq}]")
+        ws = self.workspace if workspace is None else workspace
+        B._check(B.load().hga_paged_decode(
+            self._pp, self._pc, _ints(pos, "pos", p.B), B._here(q, "q"), B._here(O, "O"), B._here(lse, "lse"),
+            None if cidx is None else _ints(cidx, "cidx", p.B, p.Hkv, wc),
+            None if gidx is None else _ints(gidx, "gidx", p.B, p.Hkv, wg),
+            None if ws is None else B._here(ws, "workspace"), 0 if ws is None else ws.numel() * ws.element_size(),
+            B._stream(stream)))
+
+
+class PagedDecodeState:
+    """Generation with HGA from a paged 8-bit cache, a batch of sequences at
+    positions of their own.
+
+    Pages are handed out in order: sequence b's chunk c gets page
+    b * max_chunks + c.  ``prefill`` appends prompts, each ``step`` appends one
+    token per sequence and attends; both rotate by ``rope`` (``rope_table``)
+    when it is given.  ``pos`` counts the tokens in the cache; ``step``
+    advances it on the device, so a step can be captured and replayed."""
+
+    def __init__(self, B_: int, Hq: int, Hkv: int, d: int, max_tokens: int, k_c: int, k_g: int, dtype: int = HGA_BF16,
+                 cache_dtype: int = HGA_INT8, scale: float = 0.0, rope=None, interleaved: bool = False,
+                 device="cuda"):
+        chunks = -(-max_tokens // 64)
+        self.p = p = PagedParams(B_, Hq, Hkv, d, B_ * chunks, chunks, k_c, k_g, dtype, cache_dtype, scale)
+        i32 = dict(device=device, dtype=torch.int32)
+        self.cache = PagedCache(p, table=torch.arange(B_ * chunks, **i32).view(B_, chunks))
+        wc, wg = paged_widths(p)
+        dense = k_c == HGA_ALL and k_g == HGA_ALL
+        self.cidx = None if dense else torch.empty(B_, Hkv, wc, **i32)
+        self.gidx = None if dense else torch.empty(B_, Hkv, wg, **i32)
+        self.O = torch.empty(B_, Hq, d, device=device, dtype=torch.float32)
+        self.lse = torch.empty(B_, Hq, device=device, dtype=torch.float32)
+        self.q = torch.empty(B_, Hq, d, device=device, dtype=p.torch_dtype)
+        self.pos = torch.zeros(B_, **i32)            # tokens in the cache
+        self.rope, self.interleaved = rope, interleaved
+
+    def prefill(self, k, v, cu, stream=None):
+        """Prompts k, v [N][Hkv][d] (unrotated), sequence b's tokens at
+        cu[b] .. cu[b + 1] - 1 (int32, device)."""
+        with torch.cuda.stream(stream or torch.cuda.current_stream()):
+            self.cache.append(self.pos, k, v, cu=cu, rope=self.rope, interleaved=self.interleaved)
+            self.pos += cu[1:] - cu[:-1]
+
+    def step(self, q, k, v, stream=None):
+        """The next token of every sequence: q [B][Hq][d], k, v [B][Hkv][d];
+        returns O [B][Hq][d] (float32, the state's buffer)."""
+        with torch.cuda.stream(stream or torch.cuda.current_stream()):
+            self.cache.append(self.pos, k, v, q=q, q_out=self.q, rope=self.rope, interleaved=self.interleaved)
+            self.cache.decode(self.pos, self.q, self.O, self.lse, self.cidx, self.gidx)
+            self.pos += 1
+        return self.O

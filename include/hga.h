@@ -68,6 +68,8 @@ extern "C" {
 
 #define HGA_BF16 0              /* Q, K, V, dO are bfloat16                  */
 #define HGA_FP32 1              /* Q, K, V, dO are float32                   */
+#define HGA_INT8 2              /* paged cache: codes -127 .. 127            */
+#define HGA_E4M3 3              /* paged cache: 8-bit floats, at most 448    */
 
 typedef void* hga_stream_t;     /* a cudaStream_t                            */
 
@@ -323,6 +325,138 @@ int hga_attn_bwd_causal(const hga_params* p, const void* Q, const void* K,
                         const int32_t* sched, float* dQ, float* dK_seg,
                         float* dV_seg, hga_stream_t stream);
 
+/* Position rotation of a training segment, and its gradient.  The article has
+ * no counterpart: these calls serve models that rotate queries and keys by
+ * their positions before the attention, between the projections' layout and
+ * the attention's.  The pair (x1, x2) of frequency i at position
+ * pos0 + t becomes
+ *     y1 = x1 c - x2 s,  y2 = x2 c + x1 s,
+ *     c = table[pos0 + t][i], s = table[pos0 + t][rot_dim / 2 + i],
+ * every product and sum rounded to float32, the result rounded once to the
+ * output's type (nearest even).  Pairs are elements (i, i + rot_dim / 2), or
+ * (2i, 2i + 1) when interleaved != 0; elements from rot_dim on pass
+ * unchanged.  rot_dim = 0 only changes layout and type (table may be NULL).
+ *   table  [table_rows][rot_dim] float32: cosines, then sines, of each
+ *          position (form the angles in float64: at position 100000 a
+ *          float32 angle is off by up to 0.004).
+ * hga_rope_fwd: x [B][T][H][d] (x_dtype, element strides x_batch, x_token,
+ *   x_head, unit stride along d) -> y [B][H][T][d] (y_dtype, dense).
+ * hga_rope_bwd: dy [B][H][T][d] (y_dtype, dense) -> dx [B][T][H][d]
+ *   (x_dtype, strided): the transposed rotation, dx1 = dy1 c + dy2 s,
+ *   dx2 = dy2 c - dy1 s.  dx rows are overwritten, not accumulated.
+ * rot_dim is a multiple of 16 and at most d; strides are non-negative and
+ * span multiples of 16 bytes; pos0 + T must not exceed table_rows; T = 0 is
+ * no work.  Input and output must not overlap. */
+typedef struct hga_rope_params {
+    int     B, H, d;             /* d in {64, 128}                           */
+    int     rot_dim, interleaved;
+    int     x_dtype, y_dtype;    /* HGA_BF16 or HGA_FP32                     */
+    int64_t T, pos0, table_rows;
+    int64_t x_batch, x_token, x_head;
+} hga_rope_params;
+
+int hga_rope_fwd(const hga_rope_params* p, const void* x, const float* table, void* y, hga_stream_t stream);
+int hga_rope_bwd(const hga_rope_params* p, const void* dy, const float* table, void* dx, hga_stream_t stream);
+
+/* Paged 8-bit cache for generation with a ragged batch (the decode step of
+ * the article's section "Retrieval: no degradation in the dense baseline";
+ * it says nothing of pages or 8 bits): the older KV of every sequence in 8
+ * bits, in pages that an allocator hands out, with lengths that live on the
+ * device, so one captured step serves every position.
+ *
+ * A page holds one complete 64-token chunk.  The chunk that a sequence is
+ * filling, and its last chunk when that is just complete, is held exactly in
+ * the sequence's open rows.
+ *   k_pages, v_pages [n_pages][Hkv][64][d]  codes (cache_dtype)
+ *   k_scale, v_scale [n_pages][Hkv][8]      float32, one for each 8-token
+ *                    group: a value is code * scale
+ *   csum, gsum       [n_pages][Hkv][d], [n_pages][Hkv][8][d]  float32 chunk
+ *                    and group summaries (means of the exact keys)
+ *   k_tail           [B][Hkv][64][d]  float32: keys of the open chunk
+ *   v_tail           [B][Hkv][64][d]  dtype: its values
+ *   table            [B][max_chunks]  int32: page of each chunk; entries of
+ *                    chunks that are not complete are not read
+ * Sequences may share the pages of complete chunks (a common prefix); a page
+ * that a call completes must belong to that sequence alone.
+ *
+ * pos, cu_tokens and table are read on the device and checked there, in
+ * every build: a page outside the pool is neither read nor written (its
+ * groups are left out), tokens past the table's width or the rotation
+ * table's rows, and sequences with token offsets outside [0, N], are
+ * skipped.  The first such fault is recorded; hga_device_check reads it. */
+typedef struct hga_paged_params {
+    int     B, Hq, Hkv, d;       /* d in {64, 128}; Hq % Hkv == 0            */
+    int     max_chunks;          /* chunks per sequence, at most             */
+    int64_t n_pages;             /* pages in the pool                        */
+    int     k_c, k_g;            /* >= 1, or HGA_ALL                         */
+    float   scale;               /* softmax scale; 0 selects 1/sqrt(d)       */
+    int     dtype;               /* q, k, v, v_tail: HGA_BF16 or HGA_FP32    */
+    int     cache_dtype;         /* HGA_INT8 or HGA_E4M3                     */
+} hga_paged_params;
+
+typedef struct hga_paged_cache {
+    void*          k_pages;
+    void*          v_pages;
+    float*         k_scale;
+    float*         v_scale;
+    float*         csum;
+    float*         gsum;
+    float*         k_tail;
+    void*          v_tail;
+    const int32_t* table;
+} hga_paged_cache;
+
+/* Append N packed tokens: sequence b gets tokens cu_tokens[b] ..
+ * cu_tokens[b + 1] - 1 at positions pos[b], pos[b] + 1, ...; pos[b] is the
+ * number of tokens that it holds (negative: an empty slot, skipped), and is
+ * not changed.  cu_tokens = NULL: one token each (N = B).  Tokens that belong
+ * to no sequence (behind cu_tokens[B]) are left alone, in q_out too.
+ *   k, v   rows [N][Hkv][d] (dtype) by element strides (token, head), unit
+ *          stride along d; q rows [N][Hq][d] alike, or NULL
+ *   q_out  [N][Hq][d] (dtype, dense): the rotated queries
+ *   rope   [rope_rows][rot_dim] as for hga_rope_fwd; rot_dim = 0: the rows
+ *          come rotated, or are not to be
+ * Keys are rotated in float32 and not rounded again.  A completed group x (8
+ * rows of one head; a = max |x|, L = 127 or 448) is held as
+ *     scale = a' / L, code = round(x * (L * (1 / a'))), a' = max(a, L 2^-126)
+ * (to nearest even); a group with a value that is not finite gets a NaN
+ * scale.  Appending tokens one by one, or all at once, leaves the same cache
+ * bit for bit. */
+int hga_paged_append(const hga_paged_params* p, const hga_paged_cache* c, const int32_t* pos,
+                     const int32_t* cu_tokens, int64_t N, const void* q, int64_t q_token, int64_t q_head,
+                     const void* k, int64_t k_token, int64_t k_head, const void* v, int64_t v_token,
+                     int64_t v_head, void* q_out, const float* rope, int64_t rope_rows, int rot_dim,
+                     int interleaved, hga_stream_t stream);
+
+/* Row widths of the index tables: wc = k_c (max_chunks for HGA_ALL); wg = k_g
+ * (8 * wc for HGA_ALL). */
+int hga_paged_widths(const hga_paged_params* p, int* wc, int* wg);
+
+/* Bytes of device scratch that hga_paged_decode needs (on the current
+ * device); 0 when none, or on invalid parameters. */
+size_t hga_paged_workspace_size(const hga_paged_params* p);
+
+/* One decode step: the query of sequence b stands at position pos[b], in the
+ * chunk of the last token that hga_paged_append has put into the cache
+ * (pos[b] is that token's position in a generation step; negative: an empty
+ * sequence, O = 0, lse = -inf, index rows -1).  As hga_decode: chunks
+ * c < pos / 64 are routed on csum with the sum of the kv-head's G queries
+ * (top k_c), then their groups on gsum (top k_g; equal scores go to the lower
+ * index), with scores formed in float64; each q-head attends the routed
+ * groups' held values and the open rows 0 .. pos % 64.  k_c = k_g = HGA_ALL
+ * is attention over the whole cache.
+ *   q     [B][Hq][d] (dtype, dense; rotated)
+ *   O     [B][Hq][d] float32;  lse [B][Hq] float32, natural log
+ *   cidx  [B][Hkv][wc], gidx [B][Hkv][wg] int32 (hga_paged_widths), written;
+ *         both may be NULL when k_c = k_g = HGA_ALL
+ *   workspace  hga_paged_workspace_size(p) bytes, 16-byte aligned; calls that
+ *         may overlap on the GPU need workspaces of their own
+ * At most 8 q-heads per kv-head; HGA_ERR_UNSUPPORTED too when the routing
+ * state of max_chunks and k_c exceeds shared memory. */
+int hga_paged_decode(const hga_paged_params* p, const hga_paged_cache* c, const int32_t* pos, const void* q,
+                     float* O, float* lse, int32_t* cidx, int32_t* gidx, void* workspace, size_t ws_bytes,
+                     hga_stream_t stream);
+
 /* Status word of the kernels' bounded waits: every wait of a tensor-core
  * kernel or of the decode kernel on a barrier gives up after one second, records the code of the wait
  * in this word and lets the kernel return (its outputs are then invalid).
@@ -341,8 +475,10 @@ int hga_device_status(int* status, int clear);
  * In that build hga_route_groups, hga_attn_fwd, hga_attn_bwd,
  * hga_attn_bwd_noalloc, hga_stage_routed, hga_attn_fwd_causal and
  * hga_attn_bwd_causal wait for their stream and return HGA_ERR_DEVICE_CHECK
- * (outputs invalid, word cleared) when a check failed.  Release builds skip
- * the checks and return without waiting.
+ * (outputs invalid, word cleared) when a check failed; hga_paged_append and
+ * hga_paged_decode, which check their device data in every build, report it
+ * so as well.  Release builds skip the other checks and return without
+ * waiting.
  * hga_checked_build: 1 in a checked build, else 0.
  * hga_device_check: *word = the first failed check's site code (0: none);
  * `clear` != 0 resets it.  Synchronises with the device. */
