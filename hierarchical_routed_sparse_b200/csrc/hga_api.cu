@@ -648,13 +648,6 @@ int hga_paged_widths(const hga_paged_params* p, int* wc, int* wg)
     return HGA_OK;
 }
 
-size_t hga_paged_workspace_size(const hga_paged_params* p)
-{
-    hga::PagedShape s{};
-    if (paged_shape(p, &s)) return 0;
-    return hga::paged_workspace(s);
-}
-
 int hga_paged_append(const hga_paged_params* p, const hga_paged_cache* c, const int32_t* pos,
                      const int32_t* cu_tokens, int64_t N, const void* q, int64_t q_token, int64_t q_head,
                      const void* k, int64_t k_token, int64_t k_head, const void* v, int64_t v_token,
@@ -696,8 +689,7 @@ int hga_paged_append(const hga_paged_params* p, const hga_paged_cache* c, const 
 }
 
 int hga_paged_decode(const hga_paged_params* p, const hga_paged_cache* c, const int32_t* pos, const void* q,
-                     float* O, float* lse, int32_t* cidx, int32_t* gidx, void* workspace, size_t ws_bytes,
-                     hga_stream_t stream)
+                     float* O, float* lse, int32_t* cidx, int32_t* gidx, hga_stream_t stream)
 {
     const NvtxRange nvtx_range("hga_paged_decode");
     hga::PagedShape s{};
@@ -717,12 +709,8 @@ int hga_paged_decode(const hga_paged_params* p, const hga_paged_cache* c, const 
             return fail(HGA_ERR_UNSUPPORTED, "routing of %d chunks / k_c=%d exceeds the kernel's shared memory",
                         s.max_chunks, s.wc);
     }
-    const size_t need = hga::paged_workspace(s);
-    if (need > 0) CHECK_PTR(workspace);
-    if (ws_bytes < need)
-        return fail(HGA_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu needed", ws_bytes, need);
     const auto st = static_cast<cudaStream_t>(stream);
-    return finish(hga::launch_paged_decode(s, *c, pos, q, O, lse, cidx, gidx, workspace, st), st, "hga_paged_decode");
+    return finish(hga::launch_paged_decode(s, *c, pos, q, O, lse, cidx, gidx, st), st, "hga_paged_decode");
 }
 
 int hga_attn_fwd(const hga_params* p, const void* Q, const void* K, const void* V,

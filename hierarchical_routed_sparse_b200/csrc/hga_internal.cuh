@@ -164,6 +164,10 @@ cudaError_t allow_smem(Kern kernel, int bytes)
     return allow_smem_fn(reinterpret_cast<const void*>(kernel), bytes);
 }
 
+// Let a kernel be launched with clusters of more than 8 CTAs (once per kernel
+// and device; tma_map.cu).
+cudaError_t allow_large_clusters(const void* kernel);
+
 // ---- launchers (each returns cudaError_t of its launch) ------------------------
 // K holds T_src rows per (batch, kv-head), the first of them at position row0.
 cudaError_t launch_summaries(const Shape& s, const void* K, int64_t T_src, int64_t row0, int64_t c_begin,
@@ -229,10 +233,8 @@ bool rope_grid_fits(const RopeShape& s);
 cudaError_t launch_paged_append(const PagedShape& s, const hga_paged_cache& c, const PagedAppend& a, cudaStream_t st);
 bool paged_append_grid_fits(const PagedShape& s, const PagedAppend& a);
 cudaError_t launch_paged_decode(const PagedShape& s, const hga_paged_cache& c, const int32_t* pos, const void* q,
-                                float* O, float* lse, int32_t* cidx, int32_t* gidx, void* workspace,
-                                cudaStream_t st);
+                                float* O, float* lse, int32_t* cidx, int32_t* gidx, cudaStream_t st);
 size_t paged_decode_smem(const PagedShape& s);
-size_t paged_workspace(const PagedShape& s);
 
 // Streaming multiprocessors of the current device (cached per device).
 int sm_count();

@@ -1,0 +1,472 @@
+// paged_attend.cuh -- one warp's attention over 16 keys at a time, for the up
+// to 8 q-heads of a kv-head.
+//
+// The products run as mma.sync m16n8k16 with the keys (scores) or the head
+// dimension (outputs) as M and the heads as N = 8: S^T = K Q^T, O^T = V^T P^T.
+// A decode step does 2 x 8 multiply-adds for each code it reads, a
+// hundredth of what tcgen05 could do and far below what its 128-row tiles
+// would have to be fed, so the tensor work must be cheap to feed, not fast:
+// with these fragments every code goes from global memory to the register
+// it is used from.  Which d an MMA's k index means and which key its column is are
+// free as long as both operands agree, so the lanes' pieces are chosen as
+// whole 16-byte loads:
+//   lane = 4 g + t (g < 8, t < 4).
+//   K   lane holds rows g of both groups, d = 64 j + 16 t .. + 15
+//   Q   lane holds head g at the same d
+//   V   lane holds rows 2t, 2t + 1 of both groups, d = (D/8) g .. + D/8 - 1
+//   S   lane gets heads 2t, 2t + 1 of rows g; O: the same heads at its V d's.
+// The weights pass from the S lanes to the P^T operand's by movmatrix.
+//
+// Precision.  Codes are exact in float16 (int8: at most 127; e4m3: 4
+// significant bits).  A bf16 query is exact in float16 too once its row is
+// scaled by a power of two (elements 2^-27 below the row's largest lose
+// bits: their products are below the sum's rounding); a float32 query, and
+// every weight, is the sum of two float16 parts, which carry 2^-24 of it.
+// Sums are float32.
+//
+// Running softmax, in units of log2.  With s the score and v the group's value
+// scale, a weight enters the products as e v, e = 2^(s - R).  The reference R
+// follows the largest s + log2 v, so that e v stays below 2^15 whatever the
+// scales are, and it moves only when that would be exceeded: R is
+// 12 below the maximum it was set from, so most tiles find it as it should
+// be and weights down to 2^-24 of the largest keep all their bits.  (Open
+// rows take the largest of their values for v, for the reference alone.)
+// The normalising sum collects e, which stays below 2^105 since log2 v counts
+// as at least -90 there; values below 2^-90 lose bits.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "hga_internal.cuh"
+
+namespace hga {
+namespace paged {
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kFloor = -1e30f;                     // R of a warp that has met no key
+constexpr float kBelow = 12.f, kAbove = 15.f;
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Transpose of an 8 x 8 matrix of 16-bit elements, two of a row in each lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t half2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+
+// Float16 pair = hi + lo of two float32 values.
+__device__ __forceinline__ void split_half2(float x0, float x1, uint32_t& hi, uint32_t& lo)
+{
+    const __half2 h = __floats2half2_rn(x0, x1);
+    const float2 f = __half22float2(h);
+    hi = half2_bits(h);
+    lo = half2_bits(__floats2half2_rn(x0 - f.x, x1 - f.y));
+}
+
+// Codes to float16.  four(): the codes of a word, two and two.
+template <int CACHE> struct Codes;
+template <> struct Codes<HGA_INT8> {
+    // 0x64 above a byte u is the float16 1024 + u; u = code + 128.
+    static __device__ __forceinline__ uint32_t prep(uint32_t w) { return w ^ 0x80808080u; }
+    static __device__ __forceinline__ uint32_t low(uint32_t u)
+    {
+        const uint32_t m = __byte_perm(u, 0x64646464u, 0x4140), k = 0x64806480u;
+        return half2_bits(__hsub2(*reinterpret_cast<const __half2*>(&m), *reinterpret_cast<const __half2*>(&k)));
+    }
+    static __device__ __forceinline__ uint32_t high(uint32_t u)
+    {
+        const uint32_t m = __byte_perm(u, 0x64646464u, 0x4342), k = 0x64806480u;
+        return half2_bits(__hsub2(*reinterpret_cast<const __half2*>(&m), *reinterpret_cast<const __half2*>(&k)));
+    }
+};
+template <> struct Codes<HGA_E4M3> {
+    static __device__ __forceinline__ uint32_t prep(uint32_t w) { return w; }
+    static __device__ __forceinline__ uint32_t low(uint32_t u)
+    {
+        uint32_t h;
+        asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;}" : "=r"(h) : "r"(u));
+        return h;
+    }
+    static __device__ __forceinline__ uint32_t high(uint32_t u)
+    {
+        uint32_t h;
+        asm("{.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, b;}" : "=r"(h) : "r"(u));
+        return h;
+    }
+};
+
+// Running state of a warp: references and sums of heads 2t, 2t + 1 (the sum
+// over this lane's rows only) and their outputs.
+template <int D> struct Running {
+    static constexpr int kM = D / 16;
+    float acc[kM][4];                                // [i]: d = (D/8) g + 2i, head 2t, 2t + 1; then d + 1
+    float R0, R1, l0, l1;
+
+    __device__ __forceinline__ void init()
+    {
+#pragma unroll
+        for (int i = 0; i < kM; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+        R0 = R1 = kFloor;
+        l0 = l1 = 0.f;
+    }
+    // Move the references up where a tile's largest s + log2 v asks for it.
+    __device__ __forceinline__ void follow(float m0, float m1)
+    {
+        if (!__any_sync(0xFFFFFFFFu, m0 > R0 + kAbove || m1 > R1 + kAbove)) return;
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+            m0 = fmaxf(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, o));
+            m1 = fmaxf(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, o));
+        }
+        const float n0 = fmaxf(R0, m0 - kBelow), n1 = fmaxf(R1, m1 - kBelow);
+        const float f0 = ex2(R0 - n0), f1 = ex2(R1 - n1);
+        R0 = n0;
+        R1 = n1;
+        l0 *= f0;
+        l1 *= f1;
+#pragma unroll
+        for (int i = 0; i < kM; ++i) {
+            acc[i][0] *= f0;
+            acc[i][1] *= f1;
+            acc[i][2] *= f0;
+            acc[i][3] *= f1;
+        }
+    }
+    // o [G][D], r [G], l [G] of this warp.
+    __device__ __forceinline__ void store(float* o, float* r, float* l, int G, int lane)
+    {
+        const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+            l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, x);
+            l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, x);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if (2 * t + e >= G) continue;
+            float* row = o + (2 * t + e) * D + (D / 8) * g;
+#pragma unroll
+            for (int i = 0; i < kM; ++i) *reinterpret_cast<float2*>(row + 2 * i) = make_float2(acc[i][e], acc[i][2 + e]);
+            if (g == 0) {
+                r[2 * t + e] = e ? R1 : R0;
+                l[2 * t + e] = e ? l1 : l0;
+            }
+        }
+    }
+};
+
+__device__ __forceinline__ void load4(const float* p, float (&y)[4])
+{
+    const float4 w = __ldg(reinterpret_cast<const float4*>(p));
+    y[0] = w.x; y[1] = w.y; y[2] = w.z; y[3] = w.w;
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&y)[4])
+{
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
+    y[0] = __uint_as_float(w.x << 16); y[1] = __uint_as_float(w.x & 0xFFFF0000u);
+    y[2] = __uint_as_float(w.y << 16); y[3] = __uint_as_float(w.y & 0xFFFF0000u);
+}
+
+// The query as the products' B operand, and what turns a product into a
+// score in log2 units, for heads 2t, 2t + 1.
+template <typename TIn, int D> struct Query {
+    static constexpr bool kTwo = sizeof(TIn) == 4;   // float32: two float16 parts
+    uint32_t b[D / 16][2], c[kTwo ? D / 16 : 1][2];
+    float f0, f1;
+
+    __device__ __forceinline__ Query(const TIn* q, int G, float scale, int lane)
+    {
+        const int g = lane >> 2, t = lane & 3;
+        float x[D / 16][4], top = 0.f;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+            {
+                float (&y)[4] = x[4 * j + k];
+                y[0] = y[1] = y[2] = y[3] = 0.f;
+                if (g < G) load4(q + g * D + 64 * j + 16 * t + 4 * k, y);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(y[e]));
+            }
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        // 2^(13 - floor(log2 top)), by the exponent's bits; 1 for rows of zeros
+        // and of infinities.
+        const int ex = int(__float_as_uint(top) >> 23);
+        const int sh = ex == 0 || ex == 255 ? 0 : min(max(13 - (ex - 127), -100), 100);
+        const float up = __uint_as_float(uint32_t(127 + sh) << 23), down = __uint_as_float(uint32_t(127 - sh) << 23);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                uint32_t lo;
+                split_half2(x[k][2 * e] * up, x[k][2 * e + 1] * up, b[k][e], lo);
+                if constexpr (kTwo) c[k][e] = lo;
+            }
+        // Head n's factor sits in the lanes of g = n.
+        f0 = __shfl_sync(0xFFFFFFFFu, down, 8 * t) * scale;
+        f1 = __shfl_sync(0xFFFFFFFFu, down, 8 * t + 4) * scale;
+    }
+};
+
+// The codes and scales of two groups; one that is missing has a scale of -1.
+template <int D> struct HeldTile {
+    uint4 k[D / 64][2];                              // rows g of the groups
+    uint2 v[4][D / 64];                              // rows 2t, 2t + 1 of the first, of the second
+    float ks0, ks1, va0, va1;                        // key scales; value scales
+
+    __device__ __forceinline__ void load(const uint8_t* kp, const uint8_t* vp, const float* ks, const float* vs, int64_t a,
+                                         int64_t z, int lane)
+    {
+        const int g = lane >> 2, t = lane & 3;
+        const bool ha = a >= 0, hz = z >= 0;
+        ks0 = ha ? __ldg(ks + a) : -1.f;
+        ks1 = hz ? __ldg(ks + z) : -1.f;
+        va0 = ha ? __ldg(vs + a) : 0.f;
+        va1 = hz ? __ldg(vs + z) : 0.f;
+        const int64_t ka = a * (kGroup * D) + g * D + 16 * t, kz = z * (kGroup * D) + g * D + 16 * t;
+        const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+            k[j][0] = ha ? __ldg(reinterpret_cast<const uint4*>(kp + ka + 64 * j)) : none;
+            k[j][1] = hz ? __ldg(reinterpret_cast<const uint4*>(kp + kz + 64 * j)) : none;
+        }
+        const int64_t ra = a * (kGroup * D) + 2 * t * D + (D / 8) * g, rz = z * (kGroup * D) + 2 * t * D + (D / 8) * g;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            if constexpr (D == 128) {
+                const uint4 x = ha ? __ldg(reinterpret_cast<const uint4*>(vp + ra + r * D)) : none;
+                const uint4 y = hz ? __ldg(reinterpret_cast<const uint4*>(vp + rz + r * D)) : none;
+                v[r][0] = make_uint2(x.x, x.y);
+                v[r][D / 64 - 1] = make_uint2(x.z, x.w);
+                v[2 + r][0] = make_uint2(y.x, y.y);
+                v[2 + r][D / 64 - 1] = make_uint2(y.z, y.w);
+            } else {
+                v[r][0] = ha ? __ldg(reinterpret_cast<const uint2*>(vp + ra + r * D)) : make_uint2(0u, 0u);
+                v[2 + r][0] = hz ? __ldg(reinterpret_cast<const uint2*>(vp + rz + r * D)) : make_uint2(0u, 0u);
+            }
+        }
+    }
+};
+
+// log2 of a positive value rounded up (or one more), for the reference only:
+// kept in [-90, 100]; 0 where the value is not finite.
+__device__ __forceinline__ float log2_above(float v)
+{
+    const int e = int(__float_as_uint(v) >> 23) - 126;
+    return e > 128 ? 0.f : (float)min(max(e, -90), 100);
+}
+
+template <typename TIn, int D, int CACHE>
+__device__ __forceinline__ void attend_held(Running<D>& run, const Query<TIn, D>& q, const HeldTile<D>& x, int lane)
+{
+    using C = Codes<CACHE>;
+    float s[4] = {0.f, 0.f, 0.f, 0.f}, r[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) {
+        const uint32_t wa[4] = {x.k[j][0].x, x.k[j][0].y, x.k[j][0].z, x.k[j][0].w};
+        const uint32_t wz[4] = {x.k[j][1].x, x.k[j][1].y, x.k[j][1].z, x.k[j][1].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t ua = C::prep(wa[k]), uz = C::prep(wz[k]);
+            const uint32_t a0 = C::low(ua), a1 = C::low(uz), a2 = C::high(ua), a3 = C::high(uz);
+            const int i = 4 * j + k;
+            mma_f16(s, a0, a1, a2, a3, q.b[i][0], q.b[i][1]);
+            if constexpr (Query<TIn, D>::kTwo) mma_f16(r, a0, a1, a2, a3, q.c[i][0], q.c[i][1]);
+        }
+    }
+    // Scores of row g of the first group (s[0], s[1]) and of the second.
+    const bool ha = !(x.ks0 < 0.f), hz = !(x.ks1 < 0.f);         // NaN scales are there
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if constexpr (Query<TIn, D>::kTwo) s[e] += r[e];
+        s[e] *= (e & 1 ? q.f1 : q.f0) * (e < 2 ? x.ks0 : x.ks1);
+        if (!(e < 2 ? ha : hz)) s[e] = -INFINITY;
+    }
+    const float la = log2_above(x.va0), lz = log2_above(x.va1);
+    run.follow(fmaxf(s[0] + la, s[2] + lz), fmaxf(s[1] + la, s[3] + lz));
+    const float e0 = ex2(s[0] - run.R0), e1 = ex2(s[1] - run.R1), e2 = ex2(s[2] - run.R0), e3 = ex2(s[3] - run.R1);
+    run.l0 += e0 + e2;
+    run.l1 += e1 + e3;
+    uint32_t ha2, la2, hz2, lz2;
+    split_half2(e0 * x.va0, e1 * x.va0, ha2, la2);
+    split_half2(e2 * x.va1, e3 * x.va1, hz2, lz2);
+    const uint32_t h0 = transpose8(ha2), h1 = transpose8(hz2), o0 = transpose8(la2), o1 = transpose8(lz2);
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t p0 = C::prep(k ? x.v[0][j].y : x.v[0][j].x), p1 = C::prep(k ? x.v[1][j].y : x.v[1][j].x);
+            const uint32_t p2 = C::prep(k ? x.v[2][j].y : x.v[2][j].x), p3 = C::prep(k ? x.v[3][j].y : x.v[3][j].x);
+            // Bytes d, d + 1 (then d + 2, d + 3) of the two keys side by side.
+            const uint32_t xa = __byte_perm(p0, p1, 0x5140), ya = __byte_perm(p0, p1, 0x7362);
+            const uint32_t xz = __byte_perm(p2, p3, 0x5140), yz = __byte_perm(p2, p3, 0x7362);
+            const int i = 4 * j + 2 * k;
+            {
+                const uint32_t a0 = C::low(xa), a1 = C::high(xa), a2 = C::low(xz), a3 = C::high(xz);
+                mma_f16(run.acc[i], a0, a1, a2, a3, h0, h1);
+                mma_f16(run.acc[i], a0, a1, a2, a3, o0, o1);
+            }
+            {
+                const uint32_t a0 = C::low(ya), a1 = C::high(ya), a2 = C::low(yz), a3 = C::high(yz);
+                mma_f16(run.acc[i + 1], a0, a1, a2, a3, h0, h1);
+                mma_f16(run.acc[i + 1], a0, a1, a2, a3, o0, o1);
+            }
+        }
+}
+
+// ---- open rows: float32 keys, values in their own type --------------------------------
+// A float32 is exactly the sum of three bfloat16 (its bits 8 and 8 and 8), so
+// products of such parts lose nothing but the terms below 2^-24 that are left
+// out.
+
+// The upper halves of two words, the first in the low half.
+__device__ __forceinline__ uint32_t upper(float x0, float x1) { return __byte_perm(__float_as_uint(x0), __float_as_uint(x1), 0x7632); }
+
+__device__ __forceinline__ void split3(float x0, float x1, uint32_t (&p)[3])
+{
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        p[i] = upper(x0, x1);
+        x0 -= __uint_as_float(p[i] << 16);
+        x1 -= __uint_as_float(p[i] & 0xFFFF0000u);
+    }
+}
+
+// Parts i of one operand and j of the other: the smallest products first.
+template <int NA, int NB, typename F> __device__ __forceinline__ void each_product(F f)
+{
+#pragma unroll
+    for (int n = 2; n >= 0; --n)
+#pragma unroll
+        for (int i = n; i >= 0; --i)
+            if (i < NA && n - i < NB) f(i, n - i);
+}
+
+// Keys row0 .. row0 + 15 of the open rows (those below `rows`).
+template <typename TIn, int D>
+__device__ __forceinline__ void attend_open(Running<D>& run, const TIn* q, int G, const float* k, const TIn* v, int row0,
+                                            int rows, float scale, int lane)
+{
+    constexpr int N = sizeof(TIn) == 4 ? 3 : 1;      // parts of q and of v
+    const int g = lane >> 2, t = lane & 3;
+    const int ra = row0 + g, rz = row0 + 8 + g;
+    const bool ha = ra < rows, hz = rz < rows;
+    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+        const int d = 64 * (i / 4) + 16 * t + 4 * (i % 4);
+        const float4 xa = ha ? __ldg(reinterpret_cast<const float4*>(k + ra * D + d)) : none;
+        const float4 xz = hz ? __ldg(reinterpret_cast<const float4*>(k + rz * D + d)) : none;
+        uint32_t a0[3], a1[3], a2[3], a3[3], b0[3], b1[3];
+        split3(xa.x, xa.y, a0);
+        split3(xz.x, xz.y, a1);
+        split3(xa.z, xa.w, a2);
+        split3(xz.z, xz.w, a3);
+        if constexpr (N == 1) {
+            const uint2 w = g < G ? __ldg(reinterpret_cast<const uint2*>(q + g * D + d)) : make_uint2(0u, 0u);
+            b0[0] = w.x;
+            b1[0] = w.y;
+        } else {
+            const float4 w = g < G ? __ldg(reinterpret_cast<const float4*>(q + g * D + d)) : none;
+            split3(w.x, w.y, b0);
+            split3(w.z, w.w, b1);
+        }
+        each_product<3, N>([&](int x, int y) { mma_bf16(s, a0[x], a1[x], a2[x], a3[x], b0[y], b1[y]); });
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] = (e < 2 ? ha : hz) ? s[e] * scale : -INFINITY;
+    uint32_t top = 0;                                // largest value of the tile: two lanes a row, 16 bytes at a time
+    if (const int row = row0 + lane / 2; row < rows) {
+        constexpr int kEach = 16 / sizeof(TIn);
+#pragma unroll
+        for (int d = 0; d < D / 2; d += kEach) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(v + row * D + (lane & 1) * (D / 2) + d));
+            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                top = max(top, x[i] & (sizeof(TIn) == 4 ? 0x7FFFFFFFu : 0x7FFF0000u));
+                if (sizeof(TIn) == 2) top = max(top, (x[i] & 0x7FFFu) << 16);
+            }
+        }
+    }
+    const float lv = log2_above(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, top)));
+    run.follow(fmaxf(s[0], s[2]) + lv, fmaxf(s[1], s[3]) + lv);
+    const float e0 = ex2(s[0] - run.R0), e1 = ex2(s[1] - run.R1), e2 = ex2(s[2] - run.R0), e3 = ex2(s[3] - run.R1);
+    run.l0 += e0 + e2;
+    run.l1 += e1 + e3;
+    uint32_t w0[3], w1[3];
+    split3(e0, e1, w0);
+    split3(e2, e3, w1);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        w0[i] = transpose8(w0[i]);
+        w1[i] = transpose8(w1[i]);
+    }
+    // Rows 2t, 2t + 1 and 8 + 2t, 8 + 2t + 1; a row that is not there counts as zero.
+    const int r0 = row0 + 2 * t;
+    const int r[4] = {r0, r0 + 1, r0 + 8, r0 + 9};
+#pragma unroll
+    for (int i = 0; i < D / 16; i += 2) {            // d = (D/8) g + 2i .. + 3
+        const int d = (D / 8) * g + 2 * i;
+        if constexpr (N == 1) {
+            uint2 w[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                w[x] = r[x] < rows ? __ldg(reinterpret_cast<const uint2*>(v + r[x] * D + d)) : make_uint2(0u, 0u);
+#pragma unroll
+            for (int x = 2; x >= 0; --x) {
+                mma_bf16(run.acc[i], __byte_perm(w[0].x, w[1].x, 0x5410), __byte_perm(w[0].x, w[1].x, 0x7632),
+                         __byte_perm(w[2].x, w[3].x, 0x5410), __byte_perm(w[2].x, w[3].x, 0x7632), w0[x], w1[x]);
+                mma_bf16(run.acc[i + 1], __byte_perm(w[0].y, w[1].y, 0x5410), __byte_perm(w[0].y, w[1].y, 0x7632),
+                         __byte_perm(w[2].y, w[3].y, 0x5410), __byte_perm(w[2].y, w[3].y, 0x7632), w0[x], w1[x]);
+            }
+        } else {
+            float4 w[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) w[x] = r[x] < rows ? __ldg(reinterpret_cast<const float4*>(v + r[x] * D + d)) : none;
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                uint32_t a0[3], a1[3], a2[3], a3[3];
+                split3(m ? w[0].z : w[0].x, m ? w[1].z : w[1].x, a0);
+                split3(m ? w[0].w : w[0].y, m ? w[1].w : w[1].y, a1);
+                split3(m ? w[2].z : w[2].x, m ? w[3].z : w[3].x, a2);
+                split3(m ? w[2].w : w[2].y, m ? w[3].w : w[3].y, a3);
+                each_product<3, 3>([&](int x, int y) { mma_bf16(run.acc[i + m], a0[x], a1[x], a2[x], a3[x], w0[y], w1[y]); });
+            }
+        }
+    }
+}
+
+}  // namespace paged
+}  // namespace hga

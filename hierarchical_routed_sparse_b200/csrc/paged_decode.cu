@@ -8,21 +8,36 @@
 // products of float32 values are exact there and a sum of 128 of them keeps
 // 2^-46, so which of two near candidates is kept is what the definition says
 // and not what an order of summation makes of it.  Every q-head attends the
-// kept groups' dequantised rows and the open rows 0 .. p % 64:
+// kept groups' held values and the open rows 0 .. p % 64:
 //     O = softmax(scale q K^T) V,  lse = log sum exp (scale q K^T).
 //
-// One CTA takes one (batch, kv-head).  Warps take keys in turn, each with a
-// running maximum and sum for each head; the warps' results meet in shared
-// memory.
-#include <cuda_fp8.h>
-
+// A cluster of S CTAs (4 warps each) takes one (batch, kv-head).
+//   * Scoring: CTA r scores the r-th part of the candidates and writes their
+//     keys into every peer's shared memory; each CTA then makes the same
+//     selection (paged_select.cuh).
+//   * Attention: a warp takes tiles of two groups (16 keys), tile i going to
+//     warp i mod 4 S of the cluster.  Codes go from global memory to the
+//     registers of mma.sync fragments without passing shared memory
+//     (paged_attend.cuh), the next tile's loads issued before the current
+//     tile's products.
+//   * Merge: every warp has a running reference, sum and unnormalised output
+//     for each head; the CTA's four meet in shared memory, and each CTA
+//     combines a 1/S part of the outputs of all S (distributed shared memory).
 #include "paged.cuh"
+#include "paged_attend.cuh"
+#include "paged_select.cuh"
+#include "sm100.cuh"
 
 namespace hga {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kMaxG = 8;
+using namespace paged;
+using sm100::cluster_rank;
+using sm100::peer_addr;
+using sm100::smem_u32;
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kMaxS = 16;                            // CTAs per (batch, kv-head)
 constexpr int kSitePage = 421, kSiteLength = 422;
 
 struct Args {
@@ -34,253 +49,342 @@ struct Args {
     float* lse;
     int32_t* cidx;
     int32_t* gidx;
+    int S;
 };
 
-// float64 scores of the chunks and of the group candidates (as ordered
-// integers), the candidates' ids and the kept rows.
+// Dynamic shared memory.  Routing: keys of the chunks, then of the group
+// candidates; the kept chunks and their pages, the kept groups and theirs.
+// The warps' outputs take the routing keys' place when these are done with;
+// what peers write (inbox) has a place of its own.
 struct Layout {
-    size_t keys, ids, crow, grow, total;
+    size_t ckeys, gkeys, crow, cpage, grow, gpage, scratch, merge, inbox, total;
 };
-__host__ __device__ inline Layout layout(const PagedShape& s)
+__host__ __device__ inline size_t up16(size_t x) { return (x + 15) & ~size_t(15); }
+__host__ __device__ inline Layout layout(const PagedShape& s, bool dense, int S)
 {
     Layout L;
-    const size_t cand = (size_t)s.wc * kGroupsPerChunk;
-    L.keys = 0;
-    L.ids = L.keys + 8 * (cand > (size_t)s.max_chunks ? cand : (size_t)s.max_chunks);
-    L.crow = L.ids + 4 * cand;
-    L.grow = L.crow + 4 * (size_t)s.wc;
-    L.total = (L.grow + 4 * (size_t)s.wg + 15) & ~size_t(15);
+    const size_t nc = dense ? 0 : (size_t)s.max_chunks, wc = dense ? 0 : (size_t)s.wc, wg = dense ? 0 : (size_t)s.wg;
+    L.ckeys = 0;
+    L.gkeys = up16(L.ckeys + 8 * nc);
+    L.scratch = up16(L.gkeys + 8 * 8 * wc);
+    L.merge = 0;
+    const size_t keys_end = L.scratch + (dense ? 0 : sizeof(SelectScratch<kWarps>));
+    const size_t merge_end = 4 * (size_t)kWarps * s.G * (s.d + 2);
+    L.crow = up16(keys_end > merge_end ? keys_end : merge_end);
+    L.cpage = L.crow + 4 * wc;
+    L.grow = L.cpage + 4 * wc;
+    L.gpage = L.grow + 4 * wg;
+    L.inbox = up16(L.gpage + 4 * wg);
+    // From each peer: 1/S of its G x d outputs, its G references and sums.
+    L.total = up16(L.inbox + 4 * ((size_t)s.G * s.d + 2 * (size_t)s.G * S));
     return L;
 }
 
-// A float64 as an integer of the same order; NaN above everything.
-__device__ __forceinline__ unsigned long long ordered(double x)
-{
-    if (x != x) return ~0ull;
-    const unsigned long long u = __double_as_longlong(x + 0.0);
-    return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ double warp_sum_f64(double v)
+template <typename TIn> __device__ __forceinline__ float widen(TIn x);
+template <> __device__ __forceinline__ float widen<float>(float x) { return x; }
+template <> __device__ __forceinline__ float widen<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// Scores of candidates [c0, c1) as ordered keys: eight lanes take a
+// candidate (four 16-byte pieces of its row each at d = 128), a warp eight
+// candidates at a time.  row(c) is null for one that cannot be read.
+template <int D, typename Row>
+__device__ __forceinline__ void score(const double* us, int c0, int c1, Row row, unsigned long long* keys, int warp,
+                                      int lane)
 {
+    constexpr int J = D / 32;
+    const int sub = lane & 7, slot = lane >> 3;
+    double u[4 * J];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    return v;
-}
-
-// Of the n keys, those that fewer than k beat (equal keys: the lower index
-// wins) in ascending order into row, -1 up to width; id(i) names candidate i.
-template <typename Id>
-__device__ __forceinline__ void select(const unsigned long long* keys, int n, int k, int32_t* row, int width, Id id,
-                                       int* count)
-{
-    __shared__ int s_base;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    __shared__ int s_warp[kWarps];
-    if (tid == 0) s_base = 0;
-    __syncthreads();
-    for (int i0 = 0; i0 < n; i0 += kThreads) {
-        const int i = i0 + tid;
-        bool keep = false;
-        if (i < n) {
-            int beat = 0;
-            if (k < n) {
-                const unsigned long long mine = keys[i];
-                for (int j = 0; j < n; ++j) beat += keys[j] > mine || (keys[j] == mine && j < i);
-            }
-            keep = beat < k;
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[4 * j + e] = us[4 * (sub + 8 * j) + e];
+    for (int base = c0 + 8 * warp; base < c1; base += 8 * kWarps) {
+        float4 x[2][J];
+        bool have[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int c = base + 4 * i + slot;
+            const float* r = c < c1 ? row(c) : nullptr;
+            have[i] = r != nullptr;
+#pragma unroll
+            for (int j = 0; j < J; ++j)
+                x[i][j] = have[i] ? __ldg(reinterpret_cast<const float4*>(r) + sub + 8 * j) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        const unsigned m = __ballot_sync(0xFFFFFFFFu, keep);
-        if (lane == 0) s_warp[warp] = __popc(m);
-        __syncthreads();
-        int at = s_base;
-        for (int w = 0; w < warp; ++w) at += s_warp[w];
-        if (keep) row[at + __popc(m & ((1u << lane) - 1u))] = id(i);
-        __syncthreads();
-        if (tid == 0)
-            for (int w = 0; w < kWarps; ++w) s_base += s_warp[w];
-        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            double a = 0.0, b = 0.0;
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                a = fma(u[4 * j], (double)x[i][j].x, a);
+                b = fma(u[4 * j + 1], (double)x[i][j].y, b);
+                a = fma(u[4 * j + 2], (double)x[i][j].z, a);
+                b = fma(u[4 * j + 3], (double)x[i][j].w, b);
+            }
+            a += b;
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+            const int c = base + 4 * i + slot;
+            if (sub == 0 && c < c1) keys[c] = ordered(have[i] ? a : -INFINITY);
+        }
     }
-    const int got = s_base;
-    for (int i = got + tid; i < width; i += kThreads) row[i] = -1;
-    if (tid == 0) *count = got;
-    __syncthreads();
 }
 
-template <int CACHE> __device__ __forceinline__ float value_of(uint8_t code)
+// keys[c0, c1) of this CTA into the same slots of its peers.
+__device__ __forceinline__ void push(unsigned long long* keys, int c0, int c1, int S, int rank, int tid)
 {
-    if constexpr (CACHE == HGA_INT8) return (float)(int8_t)code;
-    __nv_fp8_e4m3 x;
-    x.__x = code;
-    return float(x);
+    const int n = c1 - c0;
+    for (int i = tid; i < n * S; i += kThreads) {
+        const int p = i / n, c = c0 + i % n;
+        if (p != rank) sm100::st_cluster_u64(peer_addr(smem_u32(keys + c), p), keys[c]);
+    }
 }
-
-template <typename TIn> __device__ __forceinline__ float to_f32(TIn x) { return (float)x; }
-template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
 
 template <typename TIn, int D, int CACHE>
-__global__ void __launch_bounds__(kThreads) paged_decode_kernel(const __grid_constant__ Args g)
+__global__ void __launch_bounds__(kThreads, 3) paged_decode_kernel(const __grid_constant__ Args g)
 {
-    constexpr int P = D / 32;
     extern __shared__ __align__(16) uint8_t sm[];
-    const Layout L = layout(g.s);
-    auto* keys = reinterpret_cast<unsigned long long*>(sm + L.keys);
-    auto* ids = reinterpret_cast<int32_t*>(sm + L.ids);
-    auto* crow = reinterpret_cast<int32_t*>(sm + L.crow);
-    auto* grow = reinterpret_cast<int32_t*>(sm + L.grow);
     __shared__ double us[D];
-    __shared__ float pm[kWarps][kMaxG], pl[kWarps][kMaxG], po[kWarps][D];
-    __shared__ int s_nc, s_ng;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int S = g.S, rank = S > 1 ? (int)cluster_rank() : 0;
+    const int64_t bh = blockIdx.x / S;
+    const int b = int(bh / g.s.Hkv), h = int(bh % g.s.Hkv), G = g.s.G;
+    const bool dense = !g.gidx;                      // HGA_ALL without index rows
+    const Layout L = layout(g.s, dense, S);
+    if (S > 1) cluster_arrive();                     // waited for before the first write to a peer
     pdl_wait();
     pdl_trigger();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int b = blockIdx.x / g.s.Hkv, h = blockIdx.x % g.s.Hkv;
-    const int G = g.s.G;
+
     int64_t p = g.pos[b];
     if (p >= (int64_t)g.s.max_chunks * kChunk) {
-        paged::flag(kSiteLength);
+        flag(kSiteLength);
         p = -1;
     }
-    const int c0 = p < 0 ? 0 : int(p / kChunk);
-    const int rows = p < 0 ? 0 : int(p % kChunk) + 1;
+    const int64_t head0 = (int64_t)b * g.s.Hq + h * G;   // first of the kv-head's q-heads
+    if (p < 0) {                                     // an empty sequence: all CTAs of the cluster alike
+        if (rank == 0) {
+            for (int i = tid; i < G * D; i += kThreads) g.O[head0 * D + i] = 0.f;
+            for (int i = tid; i < G; i += kThreads) g.lse[head0 + i] = -INFINITY;
+            if (!dense) {
+                for (int i = tid; i < g.s.wc; i += kThreads) g.cidx[bh * g.s.wc + i] = -1;
+                for (int i = tid; i < g.s.wg; i += kThreads) g.gidx[bh * g.s.wg + i] = -1;
+            }
+        }
+        if (S > 1) cluster_wait();
+        return;
+    }
+    const int c0 = int(p / kChunk), rows = int(p % kChunk) + 1;
     const int32_t* table = g.c.table + (int64_t)b * g.s.max_chunks;
-    const TIn* q = static_cast<const TIn*>(g.q) + ((int64_t)b * g.s.Hq + h * G) * D;
+    const TIn* q = static_cast<const TIn*>(g.q) + head0 * D;
+    auto page_of = [&](int c) { return (int32_t)page_or_none(__ldg(table + c), g.s.n_pages, kSitePage); };
 
-    const bool dense = !g.gidx;                       // HGA_ALL without index rows
+    int ng = 0;
+    int32_t* gpage = reinterpret_cast<int32_t*>(sm + L.gpage);
+    int32_t* grow = reinterpret_cast<int32_t*>(sm + L.grow);
     if (!dense) {
+        auto* ckeys = reinterpret_cast<unsigned long long*>(sm + L.ckeys);
+        auto* gkeys = reinterpret_cast<unsigned long long*>(sm + L.gkeys);
+        auto* scratch = reinterpret_cast<SelectScratch<kWarps>*>(sm + L.scratch);
+        int32_t* crow = reinterpret_cast<int32_t*>(sm + L.crow);
+        int32_t* cpage = reinterpret_cast<int32_t*>(sm + L.cpage);
         for (int e = tid; e < D; e += kThreads) {
             double a = 0.0;
-            for (int i = 0; i < G; ++i) a += (double)to_f32<TIn>(q[i * D + e]);
+            for (int i = 0; i < G; ++i) a += (double)widen<TIn>(q[i * D + e]);
             us[e] = a;
         }
         __syncthreads();
-        auto score = [&](const float* row) {
-            double a = 0.0;
-#pragma unroll
-            for (int e = 0; e < P; ++e) a += us[lane * P + e] * (double)row[lane * P + e];
-            return warp_sum_f64(a);
-        };
-        const int kc = g.s.k_c > 0 ? g.s.k_c : c0;
-        if (kc < c0)
-            for (int c = warp; c < c0; c += kWarps) {
-                const int64_t page = paged::page_or_none(table[c], g.s.n_pages, kSitePage);
-                const double a = page < 0 ? -INFINITY : score(g.c.csum + (page * g.s.Hkv + h) * D);
-                if (lane == 0) keys[c] = ordered(a);
+        const int kc = g.s.k_c > 0 ? min(g.s.k_c, c0) : c0;
+        if (kc < c0) {
+            const int b0 = int((int64_t)rank * c0 / S), b1 = int((int64_t)(rank + 1) * c0 / S);
+            score<D>(us, b0, b1, [&](int c) -> const float* {
+                const int32_t page = page_of(c);
+                return page < 0 ? nullptr : g.c.csum + ((int64_t)page * g.s.Hkv + h) * D;
+            }, ckeys, warp, lane);
+            __syncthreads();
+            if (S > 1) {
+                cluster_wait();
+                push(ckeys, b0, b1, S, rank, tid);
+                cluster_arrive();
+                cluster_wait();
+                cluster_arrive();                    // for the groups' push
             }
+        }
+        select<kWarps>(ckeys, c0, kc, scratch, tid, [&](int i, int at) {
+            crow[at] = i;
+            cpage[at] = page_of(i);
+        });
         __syncthreads();
-        select(keys, c0, kc, crow, g.s.wc, [](int i) { return i; }, &s_nc);
-        const int n = s_nc * kGroupsPerChunk;
-        const int kg = g.s.k_g > 0 ? g.s.k_g : n;
-        for (int i = tid; i < n; i += kThreads) ids[i] = crow[i / kGroupsPerChunk] * kGroupsPerChunk + i % kGroupsPerChunk;
-        __syncthreads();
-        if (kg < n)
-            for (int i = warp; i < n; i += kWarps) {
-                const int64_t page = paged::page_or_none(table[ids[i] / kGroupsPerChunk], g.s.n_pages, kSitePage);
-                const double a = page < 0 ? -INFINITY
-                                          : score(g.c.gsum + ((page * g.s.Hkv + h) * kGroupsPerChunk +
-                                                              ids[i] % kGroupsPerChunk) * D);
-                if (lane == 0) keys[i] = ordered(a);
+        const int n = kc * kGroupsPerChunk;
+        const int kg = g.s.k_g > 0 ? min(g.s.k_g, n) : n;
+        if (kg < n) {
+            const int b0 = int((int64_t)rank * n / S), b1 = int((int64_t)(rank + 1) * n / S);
+            score<D>(us, b0, b1, [&](int i) -> const float* {
+                const int32_t page = cpage[i / kGroupsPerChunk];
+                return page < 0 ? nullptr
+                                : g.c.gsum + (((int64_t)page * g.s.Hkv + h) * kGroupsPerChunk + i % kGroupsPerChunk) * D;
+            }, gkeys, warp, lane);
+            __syncthreads();
+            if (S > 1) {
+                cluster_wait();
+                push(gkeys, b0, b1, S, rank, tid);
+                cluster_arrive();
+                cluster_wait();
+                cluster_arrive();                    // for the merge
             }
+        }
+        select<kWarps>(gkeys, n, kg, scratch, tid, [&](int i, int at) {
+            grow[at] = crow[i / kGroupsPerChunk] * kGroupsPerChunk + i % kGroupsPerChunk;
+            gpage[at] = cpage[i / kGroupsPerChunk];
+        });
         __syncthreads();
-        select(keys, n, kg, grow, g.s.wg, [&](int i) { return ids[i]; }, &s_ng);
-        for (int i = tid; i < g.s.wc; i += kThreads) g.cidx[(int64_t)blockIdx.x * g.s.wc + i] = crow[i];
-        for (int i = tid; i < g.s.wg; i += kThreads) g.gidx[(int64_t)blockIdx.x * g.s.wg + i] = grow[i];
+        ng = kg;
+        if (rank == 0) {
+            for (int i = tid; i < g.s.wc; i += kThreads) g.cidx[bh * g.s.wc + i] = i < kc ? crow[i] : -1;
+            for (int i = tid; i < g.s.wg; i += kThreads) g.gidx[bh * g.s.wg + i] = i < ng ? grow[i] : -1;
+        }
     }
-    const int ng = dense ? c0 * kGroupsPerChunk : s_ng;
 
-    // Keys in units of a group: the open rows first, then the kept groups.
-    float qv[kMaxG][P], acc[kMaxG][P], m[kMaxG], l[kMaxG];
-#pragma unroll
-    for (int i = 0; i < kMaxG; ++i) {
-        m[i] = -INFINITY;
-        l[i] = 0.f;
-#pragma unroll
-        for (int e = 0; e < P; ++e) {
-            qv[i][e] = i < G ? to_f32<TIn>(q[i * D + lane * P + e]) * g.s.scale : 0.f;
-            acc[i][e] = 0.f;
-        }
+    // Attention.
+    const int wid = rank * kWarps + warp, n_workers = S * kWarps;
+    Running<D> run;
+    run.init();
+    {
+        const int tiles = (rows + 15) / 16;
+        const int64_t row0 = (bh * kChunk) * D;
+        for (int i = n_workers - 1 - wid; i < tiles; i += n_workers)
+            attend_open<TIn, D>(run, q, G, g.c.k_tail + row0, static_cast<const TIn*>(g.c.v_tail) + row0, 16 * i, rows,
+                                g.s.scale * kLog2e, lane);
     }
-    auto attend = [&](const float* k, const float* v) {
-#pragma unroll
-        for (int i = 0; i < kMaxG; ++i) {
-            if (i >= G) break;
-            float a = 0.f;
-#pragma unroll
-            for (int e = 0; e < P; ++e) a = fmaf(qv[i][e], k[e], a);
-            a = warp_sum(a);
-            const float mn = fmaxf(m[i], a);
-            const float f = expf(m[i] - mn), w = expf(a - mn);
-            m[i] = mn;
-            l[i] = l[i] * f + w;
-#pragma unroll
-            for (int e = 0; e < P; ++e) acc[i][e] = fmaf(acc[i][e], f, w * v[e]);
-        }
-    };
-    const int64_t open_row = ((int64_t)b * g.s.Hkv + h) * kChunk;
-    for (int r = warp; r < rows; r += kWarps) {
-        float k[P], v[P];
-        const float* kr = g.c.k_tail + (open_row + r) * D + lane * P;
-        const TIn* vr = static_cast<const TIn*>(g.c.v_tail) + (open_row + r) * D + lane * P;
-#pragma unroll
-        for (int e = 0; e < P; ++e) {
-            k[e] = kr[e];
-            v[e] = to_f32<TIn>(vr[e]);
-        }
-        attend(k, v);
-    }
-    for (int i = warp; i < ng; i += kWarps) {
-        const int grp = dense ? i : grow[i];
-        const int64_t page = paged::page_or_none(table[grp / kGroupsPerChunk], g.s.n_pages, kSitePage);
-        if (page < 0) continue;
-        const int64_t at = (page * g.s.Hkv + h) * kGroupsPerChunk + grp % kGroupsPerChunk;
-        const float ks = g.c.k_scale[at], vs = g.c.v_scale[at];
-        const uint8_t* kr = static_cast<const uint8_t*>(g.c.k_pages) + at * kGroup * D + lane * P;
-        const uint8_t* vr = static_cast<const uint8_t*>(g.c.v_pages) + at * kGroup * D + lane * P;
-        for (int r = 0; r < kGroup; ++r) {
-            float k[P], v[P];
-#pragma unroll
-            for (int e = 0; e < P; ++e) {
-                k[e] = value_of<CACHE>(kr[r * D + e]) * ks;
-                v[e] = value_of<CACHE>(vr[r * D + e]) * vs;
+    {
+        const Query<TIn, D> qf(q, G, g.s.scale * kLog2e, lane);
+        const uint8_t* kp = static_cast<const uint8_t*>(g.c.k_pages);
+        const uint8_t* vp = static_cast<const uint8_t*>(g.c.v_pages);
+        // Group number (page, kv-head, group) of a tile's two groups, -1: none.
+        auto groups = [&](int i, int64_t& a, int64_t& z) {
+            if (dense) {
+                const int32_t page = page_of(i / 4);
+                a = page < 0 ? -1 : ((int64_t)page * g.s.Hkv + h) * kGroupsPerChunk + 2 * (i % 4);
+                z = page < 0 ? -1 : a + 1;
+            } else {
+                const int32_t pa = gpage[2 * i], pz = 2 * i + 1 < ng ? gpage[2 * i + 1] : -1;
+                a = pa < 0 ? -1 : ((int64_t)pa * g.s.Hkv + h) * kGroupsPerChunk + grow[2 * i] % kGroupsPerChunk;
+                z = pz < 0 ? -1 : ((int64_t)pz * g.s.Hkv + h) * kGroupsPerChunk + grow[2 * i + 1] % kGroupsPerChunk;
             }
-            attend(k, v);
+        };
+        const int n_tiles = dense ? 4 * c0 : (ng + 1) / 2;
+        HeldTile<D> t[2];
+        int64_t a, z;
+        int i = wid;
+        if (i < n_tiles) {
+            groups(i, a, z);
+            t[0].load(kp, vp, g.c.k_scale, g.c.v_scale, a, z, lane);
+        }
+        while (i < n_tiles) {
+            const int i1 = i + n_workers, i2 = i1 + n_workers;
+            if (i1 < n_tiles) {
+                groups(i1, a, z);
+                t[1].load(kp, vp, g.c.k_scale, g.c.v_scale, a, z, lane);
+            }
+            attend_held<TIn, D, CACHE>(run, qf, t[0], lane);
+            if (i1 >= n_tiles) break;
+            if (i2 < n_tiles) {
+                groups(i2, a, z);
+                t[0].load(kp, vp, g.c.k_scale, g.c.v_scale, a, z, lane);
+            }
+            attend_held<TIn, D, CACHE>(run, qf, t[1], lane);
+            i = i2;
         }
     }
+
+    // Merge: the CTA's warps, then the cluster's CTAs.
+    __syncthreads();                                 // the routing keys are done with
+    float* om = reinterpret_cast<float*>(sm + L.merge);          // [kWarps][G][D]
+    float* rm = om + kWarps * G * D;                             // [kWarps][G] references
+    float* lm = rm + kWarps * G;                                 // [kWarps][G] sums
+    run.store(om + warp * G * D, rm + warp * G, lm + warp * G, G, lane);
+    __syncthreads();
+    const int part = G * D / S;                      // outputs a CTA combines
+    float* inbox = reinterpret_cast<float*>(sm + L.inbox);       // [S][part], then [S][G] references, [S][G] sums
+    float* ibr = inbox + G * D;
+    float* ibl = ibr + S * G;
+    if (S > 1) {
+        // (A cluster that did not exchange keys still waits for its first arrive.)
+        cluster_wait();
+    }
+    for (int i = tid; i < G * D; i += kThreads) {
+        const int hd = i / D;
+        float M = rm[hd];
 #pragma unroll
-    for (int i = 0; i < kMaxG; ++i) {
-        if (i >= G) break;
-        if (lane == 0) {
-            pm[warp][i] = m[i];
-            pl[warp][i] = l[i];
-        }
+        for (int w = 1; w < kWarps; ++w) M = fmaxf(M, rm[w * G + hd]);
+        float o = 0.f;
 #pragma unroll
-        for (int e = 0; e < P; ++e) po[warp][lane * P + e] = acc[i][e];
-        __syncthreads();
-        float M = -INFINITY, l_all = 0.f;
-        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, pm[w][i]);
-        float f[kWarps];
-        for (int w = 0; w < kWarps; ++w) {
-            f[w] = pm[w][i] == -INFINITY ? 0.f : expf(pm[w][i] - M);
-            l_all = fmaf(pl[w][i], f[w], l_all);
+        for (int w = 0; w < kWarps; ++w) o = fmaf(om[w * G * D + i], exp2f(rm[w * G + hd] - M), o);
+        if (S > 1)
+            sm100::st_cluster_f32(peer_addr(smem_u32(inbox + rank * part + i % part), i / part), o);
+        else
+            inbox[i] = o;
+    }
+    for (int i = tid; i < G * S; i += kThreads) {
+        const int hd = i % G, to = i / G;
+        float M = rm[hd], l = 0.f;
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) M = fmaxf(M, rm[w * G + hd]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) l = fmaf(lm[w * G + hd], exp2f(rm[w * G + hd] - M), l);
+        if (S > 1) {
+            sm100::st_cluster_f32(peer_addr(smem_u32(ibr + rank * G + hd), to), M);
+            sm100::st_cluster_f32(peer_addr(smem_u32(ibl + rank * G + hd), to), l);
+        } else {
+            ibr[hd] = M;
+            ibl[hd] = l;
         }
-        const int64_t row = (int64_t)b * g.s.Hq + h * G + i;
-        for (int e = tid; e < D; e += kThreads) {
-            float o = 0.f;
-            for (int w = 0; w < kWarps; ++w) o = fmaf(po[w][e], f[w], o);
-            g.O[row * D + e] = rows > 0 ? o / l_all : 0.f;
-        }
-        if (tid == 0) g.lse[row] = rows > 0 ? M + logf(l_all) : -INFINITY;
+    }
+    if (S > 1) {
+        cluster_arrive();
+        cluster_wait();
+    } else {
         __syncthreads();
+    }
+    for (int i = tid; i < part; i += kThreads) {
+        const int e = rank * part + i, hd = e / D;
+        float M = ibr[hd];
+        for (int c = 1; c < S; ++c) M = fmaxf(M, ibr[c * G + hd]);
+        float o = 0.f, l = 0.f;
+        for (int c = 0; c < S; ++c) {
+            const float f = exp2f(ibr[c * G + hd] - M);
+            o = fmaf(inbox[c * part + i], f, o);
+            l = fmaf(ibl[c * G + hd], f, l);
+        }
+        g.O[head0 * D + e] = o / l;
+        if (e % D == 0) g.lse[head0 + hd] = (M + log2f(l)) * kLn2;
     }
 }
 
 template <typename TIn, int D, int CACHE>
 cudaError_t launch(const Args& g, cudaStream_t st)
 {
-    const size_t smem = g.gidx ? layout(g.s).total : 16;     // dense: no routing state
+    const size_t smem = layout(g.s, !g.gidx, g.S).total;
     auto k = paged_decode_kernel<TIn, D, CACHE>;
     if (cudaError_t e = allow_smem(k, (int)smem)) return e;
-    return launch_pdl(k, dim3((unsigned)(g.s.B * g.s.Hkv)), dim3(kThreads), smem, st, g);
+    if (g.S > 8)
+        if (cudaError_t e = allow_large_clusters(reinterpret_cast<const void*>(k))) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(g.s.B * g.s.Hkv * g.S));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = g.S;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = g.S > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k, g);
 }
 
 template <typename TIn, int D>
@@ -289,15 +393,25 @@ cudaError_t by_cache(const Args& g, cudaStream_t st)
     return g.s.cache_dtype == HGA_INT8 ? launch<TIn, D, HGA_INT8>(g, st) : launch<TIn, D, HGA_E4M3>(g, st);
 }
 
+// CTAs per (batch, kv-head): a power of two, as many as keep the grid within
+// what the GPU holds at once, and no more than there are chunks to share.
+int split(const PagedShape& s, bool dense)
+{
+    const int most = layout(s, dense, kMaxS).total <= 64 * 1024 ? kMaxS : 8;   // 16 CTAs must fit one GPC's SMs
+    const int64_t units = (int64_t)s.B * s.Hkv, room = (dense ? 8 : 4) * (int64_t)sm_count();
+    int S = 1;
+    while (S < most && units * S * 2 <= room && S * 4 <= s.max_chunks) S *= 2;
+    return S;
+}
+
 }  // namespace
 
-size_t paged_decode_smem(const PagedShape& s) { return layout(s).total + 8 * 1024; }
-size_t paged_workspace(const PagedShape&) { return 0; }
+size_t paged_decode_smem(const PagedShape& s) { return layout(s, false, kMaxS).total + 2048; }
 
 cudaError_t launch_paged_decode(const PagedShape& s, const hga_paged_cache& c, const int32_t* pos, const void* q,
-                                float* O, float* lse, int32_t* cidx, int32_t* gidx, void*, cudaStream_t st)
+                                float* O, float* lse, int32_t* cidx, int32_t* gidx, cudaStream_t st)
 {
-    const Args g{s, c, pos, q, O, lse, cidx, gidx};
+    const Args g{s, c, pos, q, O, lse, cidx, gidx, split(s, !gidx)};
     if (s.dtype == HGA_BF16) return s.d == 128 ? by_cache<__nv_bfloat16, 128>(g, st) : by_cache<__nv_bfloat16, 64>(g, st);
     return s.d == 128 ? by_cache<float, 128>(g, st) : by_cache<float, 64>(g, st);
 }

@@ -51,11 +51,6 @@ def paged_widths(p: PagedParams) -> tuple[int, int]:
     return wc.value, wg.value
 
 
-def paged_workspace_size(p: PagedParams) -> int:
-    """Bytes of device scratch that a decode call needs."""
-    return int(B.load().hga_paged_workspace_size(ctypes.byref(p.c())))
-
-
 def _ints(t, name, *shape):
     if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
@@ -63,11 +58,9 @@ def _ints(t, name, *shape):
 
 
 class PagedCache:
-    """The tensors of a paged cache (include/hga.h, hga_paged_cache) and the
-    scratch of its decode calls.  Tensors that are not given are allocated:
-    the pool and the open rows zeroed, the table filled with -1 (no page).
-    One cache object serves one stream at a time: its calls share the scratch
-    (the workspace that decode is given takes its place)."""
+    """The tensors of a paged cache (include/hga.h, hga_paged_cache).  Tensors
+    that are not given are allocated: the pool and the open rows zeroed, the
+    table filled with -1 (no page).  Decode calls only read the cache."""
 
     def __init__(self, p: PagedParams, device="cuda", **tensors):
         paged_widths(p)                              # the parameters are valid
@@ -95,8 +88,6 @@ class PagedCache:
         self._p, self._c = p.c(), B._PagedCache(*ptrs)
         self._pp, self._pc = ctypes.byref(self._p), ctypes.byref(self._c)
         self._widths = paged_widths(p)
-        n = paged_workspace_size(p)
-        self.workspace = torch.empty(n, dtype=torch.uint8, device=self.table.device) if n else None
 
     def _rows(self, t, name, N, H):
         if tuple(t.shape) != (N, H, self.p.d) or t.dtype != self.p.torch_dtype or t.stride(2) != 1:
@@ -127,7 +118,7 @@ class PagedCache:
             self._pp, self._pc, _ints(pos, "pos", p.B), None if cu is None else _ints(cu, "cu", p.B + 1), N, *qr, *kr,
             *vr, out, table, rows, rot, int(interleaved), B._stream(stream)))
 
-    def decode(self, pos, q, O, lse, cidx=None, gidx=None, workspace=None, stream=None):
+    def decode(self, pos, q, O, lse, cidx=None, gidx=None, stream=None):
         """The query q [B][Hq][d] of each sequence, at position pos[b] (int32,
         device; negative: empty), attends its cache: O [B][Hq][d] and lse
         [B][Hq] (float32), routing rows cidx [B][Hkv][wc], gidx [B][Hkv][wg]
@@ -140,12 +131,10 @@ class PagedCache:
             raise ValueError(f"O must be contiguous float32 [{p.B}][{p.Hq}][{p.d}]")
         if tuple(lse.shape) != (p.B, p.Hq) or lse.dtype != torch.float32 or not lse.is_contiguous():
             raise ValueError(f"lse must be contiguous float32 [{p.B}][{p.Hq}]")
-        ws = self.workspace if workspace is None else workspace
         B._check(B.load().hga_paged_decode(
             self._pp, self._pc, _ints(pos, "pos", p.B), B._here(q, "q"), B._here(O, "O"), B._here(lse, "lse"),
             None if cidx is None else _ints(cidx, "cidx", p.B, p.Hkv, wc),
             None if gidx is None else _ints(gidx, "gidx", p.B, p.Hkv, wg),
-            None if ws is None else B._here(ws, "workspace"), 0 if ws is None else ws.numel() * ws.element_size(),
             B._stream(stream)))
 
 

@@ -523,24 +523,22 @@ def test_offsets_past_32_bits():
 
 
 def test_two_streams_and_two_graphs_at_once():
-    # Calls that overlap: one cache, workspaces of their own.
+    # Calls that overlap read one cache.
     p = _params(4, 8, 2, 128, 200, 40, "bf16", "int8")
     c, q = _filled(p, "int8", [2500, 1700, 64, 0])
     pos = _int32([2499, 1699, 63, -1])
     want = _decode(c, [2499, 1699, 63, -1], q, rows=False)
-    size = max(hga.paged_workspace_size(p), 16)
     O = [torch.empty(4, 8, 128, device="cuda") for _ in range(2)]
     lse = [torch.empty(4, 8, device="cuda") for _ in range(2)]
-    ws = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(2)]
     streams = [torch.cuda.Stream() for _ in range(2)]
     graphs = []
     for i, s in enumerate(streams):
         s.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(s):
-            c.decode(pos, q, O[i], lse[i], workspace=ws[i])
+            c.decode(pos, q, O[i], lse[i])
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g, stream=s):
-            c.decode(pos, q, O[i], lse[i], workspace=ws[i])
+            c.decode(pos, q, O[i], lse[i])
         graphs.append(g)
     torch.cuda.synchronize()
     for _ in range(20):

@@ -39,9 +39,8 @@ def test_paged_params_are_refused(lib, kw, code):
     wc, wg = ctypes.c_int(), ctypes.c_int()
     assert lib.hga_paged_widths(ctypes.byref(p), ctypes.byref(wc), ctypes.byref(wg)) == code
     assert lib.hga_last_error().decode()
-    assert lib.hga_paged_workspace_size(ctypes.byref(p)) == 0
     c = B._PagedCache(*[16] * 9)
-    assert lib.hga_paged_decode(ctypes.byref(p), ctypes.byref(c), P16, P16, P16, P16, P16, P16, P16, 1 << 40, None) == code
+    assert lib.hga_paged_decode(ctypes.byref(p), ctypes.byref(c), P16, P16, P16, P16, P16, P16, None) == code
     assert _append(lib, p, c) == code
 
 
@@ -78,7 +77,7 @@ def test_cache_pointers_are_checked(lib, i):
         ptr[i] = bad
         c, p = B._PagedCache(*ptr), _paged().c()
         assert _append(lib, p, c) == BAD
-        assert lib.hga_paged_decode(ctypes.byref(p), ctypes.byref(c), P16, P16, P16, P16, P16, P16, P16, 1 << 40, None) == BAD
+        assert lib.hga_paged_decode(ctypes.byref(p), ctypes.byref(c), P16, P16, P16, P16, P16, P16, None) == BAD
 
 
 def test_append_of_nothing_is_a_no_op(lib):
@@ -88,8 +87,8 @@ def test_append_of_nothing_is_a_no_op(lib):
 def test_decode_refusals(lib):
     c = B._PagedCache(*[16] * 9)
 
-    def call(p, pos=P16, q=P16, O=P16, lse=P16, cidx=P16, gidx=P16, ws=P16, n=1 << 40):
-        return lib.hga_paged_decode(ctypes.byref(p.c()), ctypes.byref(c), pos, q, O, lse, cidx, gidx, ws, n, None)
+    def call(p, pos=P16, q=P16, O=P16, lse=P16, cidx=P16, gidx=P16):
+        return lib.hga_paged_decode(ctypes.byref(p.c()), ctypes.byref(c), pos, q, O, lse, cidx, gidx, None)
 
     for name in ("pos", "q", "O", "lse", "cidx", "gidx"):
         assert call(_paged(), **{name: None}) == BAD, name
