@@ -15,7 +15,7 @@ ragged batches; ``rope_fwd`` / ``rope_bwd`` rotate queries and keys by their
 positions.
 """
 from .pipeline import StepPipeline
-from .paged import PagedCache, PagedDecodeState, PagedParams, paged_widths
+from .paged import PagedCache, PagedDecodeState, PagedParams, paged_widths, paged_workspace_size
 from .binding import (CHECKED_LIB_PATH, EXPORTS, HGA_ALL, HGA_BF16, HGA_ERR_CUDA, HGA_ERR_DEVICE_CHECK,
                       HGA_ERR_INVALID_ARG,
                       HGA_ERR_UNSUPPORTED, HGA_FP32, HGA_OK, LIB_PATH, NOALLOC_MAX_ROWS, Buffers,
@@ -25,7 +25,7 @@ from .binding import (CHECKED_LIB_PATH, EXPORTS, HGA_ALL, HGA_BF16, HGA_ERR_CUDA
                       route_attn_fwd, route_widths, selftest_wait, stage_params, stage_routed, version, workspace_size,
                       checked_build, device_check, use_library, HGA_E4M3, HGA_INT8, rope_bwd, rope_fwd, rope_table)
 
-__all__ = ["HGA_E4M3", "HGA_INT8", "PagedCache", "PagedDecodeState", "PagedParams", "paged_widths",
+__all__ = ["HGA_E4M3", "HGA_INT8", "PagedCache", "PagedDecodeState", "PagedParams", "paged_widths", "paged_workspace_size",
            "rope_bwd", "rope_fwd", "rope_table",
            "CHECKED_LIB_PATH", "HGA_ERR_DEVICE_CHECK", "checked_build", "device_check", "use_library",
            "EXPORTS", "HGA_ALL", "HGA_BF16", "HGA_FP32", "HGA_OK", "HGA_ERR_CUDA",

@@ -30,7 +30,7 @@ EXPORTS = ("hga_route_widths", "hga_workspace_size", "hga_build_summaries", "hga
            "hga_route_groups", "hga_route", "hga_attn_fwd", "hga_route_attn_fwd", "hga_attn_bwd", "hga_attn_bwd_noalloc",
            "hga_stage_params", "hga_stage_routed", "hga_decode", "hga_route_causal", "hga_causal_sched_size",
            "hga_causal_schedule", "hga_attn_fwd_causal", "hga_attn_bwd_causal", "hga_device_status", "hga_device_check", "hga_checked_build",
-           "hga_rope_fwd", "hga_rope_bwd", "hga_paged_widths", "hga_paged_append",
+           "hga_rope_fwd", "hga_rope_bwd", "hga_paged_widths", "hga_paged_workspace_size", "hga_paged_append",
            "hga_paged_decode", "hga_selftest_wait", "hga_last_error",
            "hga_version")
 NOALLOC_MAX_ROWS = 1 << 20     # HGA_NOALLOC_MAX_ROWS
@@ -153,10 +153,11 @@ def load() -> ctypes.CDLL:
             "hga_rope_bwd": ([ctypes.POINTER(_RopeParams), P, P, P, P], ctypes.c_int),
             "hga_paged_widths": ([ctypes.POINTER(_PagedParams), ctypes.POINTER(ctypes.c_int),
                                   ctypes.POINTER(ctypes.c_int)], ctypes.c_int),
+            "hga_paged_workspace_size": ([ctypes.POINTER(_PagedParams)], ctypes.c_size_t),
             "hga_paged_append": ([ctypes.POINTER(_PagedParams), ctypes.POINTER(_PagedCache), P, P, I64, P, I64, I64,
                                   P, I64, I64, P, I64, I64, P, P, I64, ctypes.c_int, ctypes.c_int, P], ctypes.c_int),
-            "hga_paged_decode": ([ctypes.POINTER(_PagedParams), ctypes.POINTER(_PagedCache), P, P, P, P, P, P, P],
-                                 ctypes.c_int),
+            "hga_paged_decode": ([ctypes.POINTER(_PagedParams), ctypes.POINTER(_PagedCache), P, P, P, P, P, P, P,
+                                  ctypes.c_size_t, P], ctypes.c_int),
             "hga_device_status": ([ctypes.POINTER(ctypes.c_int), ctypes.c_int], ctypes.c_int),
             "hga_selftest_wait": ([ctypes.c_int, ctypes.POINTER(ctypes.c_int), P], ctypes.c_int),
             "hga_device_check": ([ctypes.POINTER(ctypes.c_int), ctypes.c_int], ctypes.c_int),
@@ -369,11 +370,11 @@ def attn_bwd_causal(p: Params, Q, K, V, O, lse, dO, gidx, dQ, dK_seg, dV_seg, st
 _HGA_DTYPE = {torch.bfloat16: HGA_BF16, torch.float32: HGA_FP32}
 
 
-def _here(t: torch.Tensor, name: str) -> int:
+def _here(t: torch.Tensor, name: str, dev: int | None = None) -> int:
     """Data pointer of a tensor on the current device (kernels run there)."""
     if not t.is_cuda:
         raise ValueError("libhga takes device tensors")
-    if t.get_device() != torch.cuda.current_device():
+    if t.get_device() != (torch.cuda.current_device() if dev is None else dev):
         raise ValueError(f"{name} is on device {t.get_device()}, the current device is {torch.cuda.current_device()}")
     return t.data_ptr()
 
@@ -395,6 +396,14 @@ def rope_table(rows: int, rot_dim: int, base: float = 10000.0, device="cuda") ->
     return torch.cat([a.cos(), a.sin()], 1).float()
 
 
+def _raw_stream(stream, dev: int) -> int:
+    """The stream's handle; the current stream's when none is given (without
+    building a Stream object: decode steps are shorter than that)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream.cuda_stream
+
+
 def _check_table(table, name: str) -> None:
     if table.dtype != torch.float32 or table.dim() != 2 or not table.is_contiguous():
         raise ValueError(f"{name} must be a contiguous float32 [rows][rot_dim] tensor")
@@ -404,17 +413,17 @@ def _rope(call, src, dst, x, y, table, pos0: int, interleaved: bool, stream) -> 
     if x.dim() != 4 or y.dim() != 4 or x.stride(3) != 1 or not y.is_contiguous():
         raise ValueError("rope takes [B][T][H][d] rows with unit stride along d and a contiguous [B][H][T][d]")
     B_, T, H, d = x.shape
-    if tuple(y.shape) != (B_, H, T, d):
+    if y.shape != (B_, H, T, d):
         raise ValueError(f"shapes {tuple(x.shape)} and {tuple(y.shape)} are not [B][T][H][d] and [B][H][T][d]")
-    rot = rows = 0
+    dev = torch.cuda.current_device() if src.is_cuda else None
+    rot, rows, tab = 0, 0, None
     if table is not None:
         _check_table(table, "table")
         rows, rot = table.shape
-    xs = x.stride()
-    p = _RopeParams(B_, H, d, rot, int(interleaved), _hga_dtype(x, "x"), _hga_dtype(y, "y"), T, pos0, rows, xs[0],
-                    xs[1], xs[2])
-    _check(call(ctypes.byref(p), _here(src, "the input"), None if table is None else _here(table, "table"),
-                _here(dst, "the output"), _stream(stream)))
+        tab = _here(table, "table", dev)
+    sb, st, sh, _ = x.stride()
+    p = _RopeParams(B_, H, d, rot, interleaved, _hga_dtype(x, "x"), _hga_dtype(y, "y"), T, pos0, rows, sb, st, sh)
+    _check(call(p, _here(src, "the input", dev), tab, _here(dst, "the output", dev), _raw_stream(stream, dev)))
 
 
 def rope_fwd(x, y, table, pos0: int = 0, interleaved: bool = False, stream=None) -> None:

@@ -56,7 +56,8 @@ int read_check_words(bool clear)
     int (*const readers[])(bool) = {hga::check_word_attn_tc_fwd, hga::check_word_attn_tc_bwd,
                                     hga::check_word_attn_simt,   hga::check_word_causal,
                                     hga::check_word_router,      hga::check_word_stage,
-                                    hga::check_word_paged_append, hga::check_word_paged_decode};
+                                    hga::check_word_paged_append, hga::check_word_paged_routed,
+                                    hga::check_word_paged_dense};
     int first = 0;
     for (auto f : readers) {
         const int v = f(clear);
@@ -648,6 +649,13 @@ int hga_paged_widths(const hga_paged_params* p, int* wc, int* wg)
     return HGA_OK;
 }
 
+size_t hga_paged_workspace_size(const hga_paged_params* p)
+{
+    hga::PagedShape s{};
+    if (paged_shape(p, &s)) return 0;
+    return s.k_c > 0 || s.k_g > 0 ? 0 : hga::paged_dense_workspace(s);
+}
+
 int hga_paged_append(const hga_paged_params* p, const hga_paged_cache* c, const int32_t* pos,
                      const int32_t* cu_tokens, int64_t N, const void* q, int64_t q_token, int64_t q_head,
                      const void* k, int64_t k_token, int64_t k_head, const void* v, int64_t v_token,
@@ -689,7 +697,8 @@ int hga_paged_append(const hga_paged_params* p, const hga_paged_cache* c, const 
 }
 
 int hga_paged_decode(const hga_paged_params* p, const hga_paged_cache* c, const int32_t* pos, const void* q,
-                     float* O, float* lse, int32_t* cidx, int32_t* gidx, hga_stream_t stream)
+                     float* O, float* lse, int32_t* cidx, int32_t* gidx, void* workspace, size_t ws_bytes,
+                     hga_stream_t stream)
 {
     const NvtxRange nvtx_range("hga_paged_decode");
     hga::PagedShape s{};
@@ -702,15 +711,20 @@ int hga_paged_decode(const hga_paged_params* p, const hga_paged_cache* c, const 
     CHECK_PTR(q);
     CHECK_PTR(O);
     CHECK_PTR(lse);
+    const auto st = static_cast<cudaStream_t>(stream);
     if (cidx || gidx || s.k_c > 0 || s.k_g > 0) {
         CHECK_PTR(cidx);
         CHECK_PTR(gidx);
-        if (hga::paged_decode_smem(s) > kMaxSmem)
+        if (hga::paged_routed_smem(s) > kMaxSmem)
             return fail(HGA_ERR_UNSUPPORTED, "routing of %d chunks / k_c=%d exceeds the kernel's shared memory",
                         s.max_chunks, s.wc);
+        return finish(hga::launch_paged_routed(s, *c, pos, q, O, lse, cidx, gidx, st), st, "hga_paged_decode");
     }
-    const auto st = static_cast<cudaStream_t>(stream);
-    return finish(hga::launch_paged_decode(s, *c, pos, q, O, lse, cidx, gidx, st), st, "hga_paged_decode");
+    CHECK_PTR(workspace);
+    const size_t need = hga::paged_dense_workspace(s);
+    if (ws_bytes < need)
+        return fail(HGA_ERR_INVALID_ARG, "workspace of %zu bytes is smaller than the %zu needed", ws_bytes, need);
+    return finish(hga::launch_paged_dense(s, *c, pos, q, O, lse, workspace, st), st, "hga_paged_decode");
 }
 
 int hga_attn_fwd(const hga_params* p, const void* Q, const void* K, const void* V,

@@ -38,7 +38,8 @@ struct RopeShape {
     int x_dtype, y_dtype;
 };
 
-// Validated shape of the paged cache's calls (paged_append.cu, paged_decode.cu).
+// Validated shape of the paged cache's calls (paged_append.cu, paged_decode.cu,
+// paged_dense.cu).
 struct PagedShape {
     int B, Hq, Hkv, G, d;
     int64_t n_pages;
@@ -195,7 +196,8 @@ int check_word_causal(bool clear);
 int check_word_router(bool clear);
 int check_word_stage(bool clear);
 int check_word_paged_append(bool clear);
-int check_word_paged_decode(bool clear);
+int check_word_paged_routed(bool clear);
+int check_word_paged_dense(bool clear);
 int selftest_status(bool clear); // status word of selftest.cu
 int selftest_site();             // the code its wait records
 cudaError_t launch_selftest_wait(unsigned long long limit_ns, cudaStream_t st);
@@ -229,12 +231,16 @@ cudaError_t launch_attn_bwd_simt(const Shape& s, const void* Q, const void* K, c
 cudaError_t launch_rope(const RopeShape& s, bool back, const void* src, const float* table, void* dst,
                         cudaStream_t st);
 bool rope_grid_fits(const RopeShape& s);
-// Paged cache (paged_append.cu, paged_decode.cu).
+// Paged cache (paged_append.cu, paged_decode.cu,
+// paged_dense.cu).
 cudaError_t launch_paged_append(const PagedShape& s, const hga_paged_cache& c, const PagedAppend& a, cudaStream_t st);
 bool paged_append_grid_fits(const PagedShape& s, const PagedAppend& a);
-cudaError_t launch_paged_decode(const PagedShape& s, const hga_paged_cache& c, const int32_t* pos, const void* q,
+cudaError_t launch_paged_routed(const PagedShape& s, const hga_paged_cache& c, const int32_t* pos, const void* q,
                                 float* O, float* lse, int32_t* cidx, int32_t* gidx, cudaStream_t st);
-size_t paged_decode_smem(const PagedShape& s);
+size_t paged_routed_smem(const PagedShape& s);
+cudaError_t launch_paged_dense(const PagedShape& s, const hga_paged_cache& c, const int32_t* pos, const void* q,
+                               float* O, float* lse, void* workspace, cudaStream_t st);
+size_t paged_dense_workspace(const PagedShape& s);
 
 // Streaming multiprocessors of the current device (cached per device).
 int sm_count();

@@ -6,16 +6,23 @@
 // A decode step does 2 x 8 multiply-adds for each code it reads, a
 // hundredth of what tcgen05 could do and far below what its 128-row tiles
 // would have to be fed, so the tensor work must be cheap to feed, not fast:
-// with these fragments every code goes from global memory to the register
-// it is used from.  Which d an MMA's k index means and which key its column is are
-// free as long as both operands agree, so the lanes' pieces are chosen as
-// whole 16-byte loads:
+// with these fragments a code is loaded from shared memory once, straight into
+// the register it is used from.  Which d an MMA's k index means and which key
+// its column is are free as long as both operands agree, so the lanes' pieces
+// are chosen as whole 16-byte loads:
 //   lane = 4 g + t (g < 8, t < 4).
-//   K   lane holds rows g of both groups, d = 64 j + 16 t .. + 15
+//   K   lane takes rows g of both groups, d = 64 j + 16 t .. + 15
 //   Q   lane holds head g at the same d
-//   V   lane holds rows 2t, 2t + 1 of both groups, d = (D/8) g .. + D/8 - 1
+//   V   lane takes rows 2t, 2t + 1 of both groups, d = (D/8) g .. + D/8 - 1
 //   S   lane gets heads 2t, 2t + 1 of rows g; O: the same heads at its V d's.
 // The weights pass from the S lanes to the P^T operand's by movmatrix.
+//
+// A tile is four groups (32 keys), two such products side by side.  Its keys
+// and its values wait in halves of the warp's own ring of shared memory,
+// filled by cp.async: while the scores of tile i are formed, its values and
+// the keys of tile i + 1 are on their way.  A warp orders its ring by itself,
+// so the loop has no barrier.  Rows of 128 bytes are swizzled so that neither
+// the K nor the V loads meet bank conflicts.
 //
 // Precision.  Codes are exact in float16 (int8: at most 127; e4m3: 4
 // significant bits).  A bf16 query is exact in float16 too once its row is
@@ -160,6 +167,28 @@ template <int D> struct Running {
             acc[i][3] *= f1;
         }
     }
+    // Out of the registers into shared memory (kParked floats), and back.
+    static constexpr int kParked = 32 * (4 * kM + 4);
+    __device__ __forceinline__ void park(float* p, int lane) const
+    {
+#pragma unroll
+        for (int i = 0; i < 4 * kM; ++i) p[32 * i + lane] = acc[i / 4][i % 4];
+        p += 32 * 4 * kM + lane;
+        p[0] = R0;
+        p[32] = R1;
+        p[64] = l0;
+        p[96] = l1;
+    }
+    __device__ __forceinline__ void unpark(const float* p, int lane)
+    {
+#pragma unroll
+        for (int i = 0; i < 4 * kM; ++i) acc[i / 4][i % 4] = p[32 * i + lane];
+        p += 32 * 4 * kM + lane;
+        R0 = p[0];
+        R1 = p[32];
+        l0 = p[64];
+        l1 = p[96];
+    }
     // o [G][D], r [G], l [G] of this warp.
     __device__ __forceinline__ void store(float* o, float* r, float* l, int G, int lane)
     {
@@ -238,45 +267,61 @@ template <typename TIn, int D> struct Query {
     }
 };
 
-// The codes and scales of two groups; one that is missing has a scale of -1.
-template <int D> struct HeldTile {
-    uint4 k[D / 64][2];                              // rows g of the groups
-    uint2 v[4][D / 64];                              // rows 2t, 2t + 1 of the first, of the second
-    float ks0, ks1, va0, va1;                        // key scales; value scales
-
-    __device__ __forceinline__ void load(const uint8_t* kp, const uint8_t* vp, const float* ks, const float* vs, int64_t a,
-                                         int64_t z, int lane)
-    {
-        const int g = lane >> 2, t = lane & 3;
-        const bool ha = a >= 0, hz = z >= 0;
-        ks0 = ha ? __ldg(ks + a) : -1.f;
-        ks1 = hz ? __ldg(ks + z) : -1.f;
-        va0 = ha ? __ldg(vs + a) : 0.f;
-        va1 = hz ? __ldg(vs + z) : 0.f;
-        const int64_t ka = a * (kGroup * D) + g * D + 16 * t, kz = z * (kGroup * D) + g * D + 16 * t;
-        const uint4 none = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int j = 0; j < D / 64; ++j) {
-            k[j][0] = ha ? __ldg(reinterpret_cast<const uint4*>(kp + ka + 64 * j)) : none;
-            k[j][1] = hz ? __ldg(reinterpret_cast<const uint4*>(kp + kz + 64 * j)) : none;
-        }
-        const int64_t ra = a * (kGroup * D) + 2 * t * D + (D / 8) * g, rz = z * (kGroup * D) + 2 * t * D + (D / 8) * g;
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            if constexpr (D == 128) {
-                const uint4 x = ha ? __ldg(reinterpret_cast<const uint4*>(vp + ra + r * D)) : none;
-                const uint4 y = hz ? __ldg(reinterpret_cast<const uint4*>(vp + rz + r * D)) : none;
-                v[r][0] = make_uint2(x.x, x.y);
-                v[r][D / 64 - 1] = make_uint2(x.z, x.w);
-                v[2 + r][0] = make_uint2(y.x, y.y);
-                v[2 + r][D / 64 - 1] = make_uint2(y.z, y.w);
-            } else {
-                v[r][0] = ha ? __ldg(reinterpret_cast<const uint2*>(vp + ra + r * D)) : make_uint2(0u, 0u);
-                v[2 + r][0] = hz ? __ldg(reinterpret_cast<const uint2*>(vp + rz + r * D)) : make_uint2(0u, 0u);
-            }
-        }
-    }
+// Half of a tile's data: the codes and scales of the keys, or of the values, of
+// four groups.  A group that is missing has a scale of -1 (keys) or 0.
+constexpr int kTileGroups = 4, kTileKeys = kTileGroups * kGroup;
+constexpr int kHalves = 3;                           // halves in a warp's ring
+template <int D> struct alignas(16) Half {
+    uint8_t code[kTileKeys * D];
+    float scale[kTileGroups];
 };
+
+// 16-byte pieces of a row change places: K by the row's parity (eight lanes
+// read four pieces of two neighbouring rows), V by the row pair (four lanes
+// read the same two pieces of rows 0, 2, 4, 6).
+template <int D, bool V> __device__ __forceinline__ int piece(int row, int c)
+{
+    if (V) return D == 128 ? c ^ (2 * ((row >> 1) & 3)) : c ^ ((row >> 1) & 3);
+    return D == 128 ? c ^ (4 * (row & 1)) : c;
+}
+
+__device__ __forceinline__ void cp16(void* dst, const void* src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(there ? 16 : 0)
+                 : "memory");
+}
+
+// Start the copy of a half: lanes 8 x .. 8 x + 7 copy group x, whose number
+// (over page, kv-head and group; -1: none) they hold in `at`.
+template <int D, bool V>
+__device__ __forceinline__ void fetch(Half<D>& s, const uint8_t* codes, const float* scales, int64_t at, int lane)
+{
+    constexpr int kPieces = D / 16, kRows = 8 / kPieces;         // pieces of a row; rows that 8 lanes copy at once
+    const int x = lane >> 3, c = lane & 7;
+    const bool there = at >= 0;
+    const uint8_t* from = codes + (there ? at : 0) * (kGroup * D) + 16 * c;
+#pragma unroll
+    for (int m = 0; m < kGroup / kRows; ++m) {
+        const int row = kRows * m + c / kPieces;
+        cp16(s.code + (kGroup * x + row) * D + 16 * piece<D, V>(row, c % kPieces), from + m * 128, there);
+    }
+    if (c == 0) {
+        if (there)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(s.scale + x)),
+                         "l"(scales + at)
+                         : "memory");
+        else
+            s.scale[x] = V ? 0.f : -1.f;
+    }
+}
+__device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All of the warp's copies but the newest two halves have landed, for all its lanes.
+__device__ __forceinline__ void fetch_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(kHalves - 1) : "memory");
+    __syncwarp();
+}
 
 // log2 of a positive value rounded up (or one more), for the reference only:
 // kept in [-90, 100]; 0 where the value is not finite.
@@ -286,62 +331,166 @@ __device__ __forceinline__ float log2_above(float v)
     return e > 128 ? 0.f : (float)min(max(e, -90), 100);
 }
 
+// Scores of a tile in log2 units: s[x][0..1] of row g of group 2x for heads 2t,
+// 2t + 1, s[x][2..3] of group 2x + 1.
 template <typename TIn, int D, int CACHE>
-__device__ __forceinline__ void attend_held(Running<D>& run, const Query<TIn, D>& q, const HeldTile<D>& x, int lane)
+__device__ __forceinline__ void held_scores(float (&s)[2][4], const Query<TIn, D>& q, const Half<D>& k, int lane)
 {
     using C = Codes<CACHE>;
-    float s[4] = {0.f, 0.f, 0.f, 0.f}, r[4] = {0.f, 0.f, 0.f, 0.f};
+    const int g = lane >> 2, t = lane & 3;
+    float r[2][4];                                   // two chains of products for each half of the tile
 #pragma unroll
-    for (int j = 0; j < D / 64; ++j) {
-        const uint32_t wa[4] = {x.k[j][0].x, x.k[j][0].y, x.k[j][0].z, x.k[j][0].w};
-        const uint32_t wz[4] = {x.k[j][1].x, x.k[j][1].y, x.k[j][1].z, x.k[j][1].w};
+    for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t ua = C::prep(wa[k]), uz = C::prep(wz[k]);
-            const uint32_t a0 = C::low(ua), a1 = C::low(uz), a2 = C::high(ua), a3 = C::high(uz);
-            const int i = 4 * j + k;
-            mma_f16(s, a0, a1, a2, a3, q.b[i][0], q.b[i][1]);
-            if constexpr (Query<TIn, D>::kTwo) mma_f16(r, a0, a1, a2, a3, q.c[i][0], q.c[i][1]);
-        }
-    }
-    // Scores of row g of the first group (s[0], s[1]) and of the second.
-    const bool ha = !(x.ks0 < 0.f), hz = !(x.ks1 < 0.f);         // NaN scales are there
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        if constexpr (Query<TIn, D>::kTwo) s[e] += r[e];
-        s[e] *= (e & 1 ? q.f1 : q.f0) * (e < 2 ? x.ks0 : x.ks1);
-        if (!(e < 2 ? ha : hz)) s[e] = -INFINITY;
-    }
-    const float la = log2_above(x.va0), lz = log2_above(x.va1);
-    run.follow(fmaxf(s[0] + la, s[2] + lz), fmaxf(s[1] + la, s[3] + lz));
-    const float e0 = ex2(s[0] - run.R0), e1 = ex2(s[1] - run.R1), e2 = ex2(s[2] - run.R0), e3 = ex2(s[3] - run.R1);
-    run.l0 += e0 + e2;
-    run.l1 += e1 + e3;
-    uint32_t ha2, la2, hz2, lz2;
-    split_half2(e0 * x.va0, e1 * x.va0, ha2, la2);
-    split_half2(e2 * x.va1, e3 * x.va1, hz2, lz2);
-    const uint32_t h0 = transpose8(ha2), h1 = transpose8(hz2), o0 = transpose8(la2), o1 = transpose8(lz2);
+        for (int e = 0; e < 4; ++e) s[x][e] = r[x][e] = 0.f;
 #pragma unroll
     for (int j = 0; j < D / 64; ++j)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const uint32_t p0 = C::prep(k ? x.v[0][j].y : x.v[0][j].x), p1 = C::prep(k ? x.v[1][j].y : x.v[1][j].x);
-            const uint32_t p2 = C::prep(k ? x.v[2][j].y : x.v[2][j].x), p3 = C::prep(k ? x.v[3][j].y : x.v[3][j].x);
-            // Bytes d, d + 1 (then d + 2, d + 3) of the two keys side by side.
-            const uint32_t xa = __byte_perm(p0, p1, 0x5140), ya = __byte_perm(p0, p1, 0x7362);
-            const uint32_t xz = __byte_perm(p2, p3, 0x5140), yz = __byte_perm(p2, p3, 0x7362);
-            const int i = 4 * j + 2 * k;
-            {
-                const uint32_t a0 = C::low(xa), a1 = C::high(xa), a2 = C::low(xz), a3 = C::high(xz);
-                mma_f16(run.acc[i], a0, a1, a2, a3, h0, h1);
-                mma_f16(run.acc[i], a0, a1, a2, a3, o0, o1);
-            }
-            {
-                const uint32_t a0 = C::low(ya), a1 = C::high(ya), a2 = C::low(yz), a3 = C::high(yz);
-                mma_f16(run.acc[i + 1], a0, a1, a2, a3, h0, h1);
-                mma_f16(run.acc[i + 1], a0, a1, a2, a3, o0, o1);
+        for (int x = 0; x < 2; ++x) {
+            const uint8_t* row = k.code + (16 * x + g) * D + 16 * piece<D, false>(g, 4 * j + t);
+            const uint4 ka = *reinterpret_cast<const uint4*>(row), kz = *reinterpret_cast<const uint4*>(row + 8 * D);
+            const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wz[4] = {kz.x, kz.y, kz.z, kz.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t ua = C::prep(wa[i]), uz = C::prep(wz[i]);
+                const uint32_t a0 = C::low(ua), a1 = C::low(uz), a2 = C::high(ua), a3 = C::high(uz);
+                mma_f16(i & 1 ? r[x] : s[x], a0, a1, a2, a3, q.b[4 * j + i][0], q.b[4 * j + i][1]);
+                if constexpr (Query<TIn, D>::kTwo)
+                    mma_f16(i & 1 ? s[x] : r[x], a0, a1, a2, a3, q.c[4 * j + i][0], q.c[4 * j + i][1]);
             }
         }
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const float ks = k.scale[2 * x + y];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                s[x][2 * y + e] = (s[x][2 * y + e] + r[x][2 * y + e]) * ((e ? q.f1 : q.f0) * ks);
+                if (ks < 0.f) s[x][2 * y + e] = -INFINITY;       // (a NaN scale is there)
+            }
+        }
+}
+
+// The tile's weights and outputs, given its scores.
+template <int D, int CACHE>
+__device__ __forceinline__ void held_outputs(Running<D>& run, const float (&s)[2][4], const Half<D>& v, int lane)
+{
+    using C = Codes<CACHE>;
+    const int g = lane >> 2, t = lane & 3;
+    float vs[4], m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+        vs[y] = v.scale[y];
+        const float lv = log2_above(vs[y]);
+        m0 = fmaxf(m0, s[y / 2][2 * (y % 2)] + lv);
+        m1 = fmaxf(m1, s[y / 2][2 * (y % 2) + 1] + lv);
+    }
+    run.follow(m0, m1);
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+        const float e0 = ex2(s[y / 2][2 * (y % 2)] - run.R0), e1 = ex2(s[y / 2][2 * (y % 2) + 1] - run.R1);
+        run.l0 += e0;
+        run.l1 += e1;
+        split_half2(e0 * vs[y], e1 * vs[y], hi[y], lo[y]);
+        hi[y] = transpose8(hi[y]);
+        lo[y] = transpose8(lo[y]);
+    }
+    // The tile's outputs are formed from zero and then added: a tensor-core sum
+    // cuts its last bit off, which over thousands of keys would show.  p: the
+    // words of rows 2t, 2t + 1 of the four groups at d .. d + 3.
+    auto four = [&](int i, const uint32_t (&p)[4][2]) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            // Bytes d, d + 1 (then d + 2, d + 3) of two keys side by side.
+            uint32_t w[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) w[y] = __byte_perm(C::prep(p[y][0]), C::prep(p[y][1]), m ? 0x7362 : 0x5140);
+            uint32_t a[2][4];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                a[x][0] = C::low(w[2 * x]);
+                a[x][1] = C::high(w[2 * x]);
+                a[x][2] = C::low(w[2 * x + 1]);
+                a[x][3] = C::high(w[2 * x + 1]);
+            }
+            float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int x = 0; x < 2; ++x) mma_f16(o, a[x][0], a[x][1], a[x][2], a[x][3], lo[2 * x], lo[2 * x + 1]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) mma_f16(o, a[x][0], a[x][1], a[x][2], a[x][3], hi[2 * x], hi[2 * x + 1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) run.acc[i + m][e] += o[e];
+        }
+    };
+    // A lane's piece of a row: D/8 bytes.
+    const int c = D == 128 ? 16 * piece<D, true>(2 * t, g) : 16 * piece<D, true>(2 * t, g / 2) + 8 * (g % 2);
+    const uint8_t* row = v.code + 2 * t * D + c;
+    if constexpr (D == 128) {
+        uint4 w[4][2];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) w[y / 2][y % 2] = *reinterpret_cast<const uint4*>(row + (8 * (y / 2) + y % 2) * D);
+        const uint32_t p0[4][2] = {{w[0][0].x, w[0][1].x}, {w[1][0].x, w[1][1].x}, {w[2][0].x, w[2][1].x}, {w[3][0].x, w[3][1].x}};
+        const uint32_t p1[4][2] = {{w[0][0].y, w[0][1].y}, {w[1][0].y, w[1][1].y}, {w[2][0].y, w[2][1].y}, {w[3][0].y, w[3][1].y}};
+        const uint32_t p2[4][2] = {{w[0][0].z, w[0][1].z}, {w[1][0].z, w[1][1].z}, {w[2][0].z, w[2][1].z}, {w[3][0].z, w[3][1].z}};
+        const uint32_t p3[4][2] = {{w[0][0].w, w[0][1].w}, {w[1][0].w, w[1][1].w}, {w[2][0].w, w[2][1].w}, {w[3][0].w, w[3][1].w}};
+        four(0, p0);
+        four(2, p1);
+        four(4, p2);
+        four(6, p3);
+    } else {
+        uint2 w[4][2];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) w[y / 2][y % 2] = *reinterpret_cast<const uint2*>(row + (8 * (y / 2) + y % 2) * D);
+        const uint32_t p0[4][2] = {{w[0][0].x, w[0][1].x}, {w[1][0].x, w[1][1].x}, {w[2][0].x, w[2][1].x}, {w[3][0].x, w[3][1].x}};
+        const uint32_t p1[4][2] = {{w[0][0].y, w[0][1].y}, {w[1][0].y, w[1][1].y}, {w[2][0].y, w[2][1].y}, {w[3][0].y, w[3][1].y}};
+        four(0, p0);
+        four(2, p1);
+    }
+}
+
+// Attention over n tiles of held keys: group_of(i) is the number of this
+// lane's group (lane / 8) of tile i, called once for each i in order by the
+// whole warp.  Halves K0 V0 K1 V1 ... go round the ring; a copy that is not
+// wanted is an empty group, so that the count of groups says what has landed.
+template <typename TIn, int D, int CACHE, typename GroupOf>
+__device__ __forceinline__ void attend_tiles(Running<D>& run, Half<D>* ring, int n, GroupOf group_of, const TIn* q, int G,
+                                             float scale, const hga_paged_cache& c, int lane)
+{
+    if (n <= 0) return;
+    const auto* kp = static_cast<const uint8_t*>(c.k_pages);
+    const auto* vp = static_cast<const uint8_t*>(c.v_pages);
+    int64_t at = group_of(0);
+    fetch<D, false>(ring[0], kp, c.k_scale, at, lane);
+    fetch_commit();
+    fetch<D, true>(ring[1], vp, c.v_scale, at, lane);
+    fetch_commit();
+    if (n > 1) {
+        at = group_of(1);
+        fetch<D, false>(ring[2], kp, c.k_scale, at, lane);
+    }
+    fetch_commit();
+    const Query<TIn, D> qf(q, G, scale, lane);
+    int slot = 0;                                    // of K_i; V_i is in the next
+    for (int i = 0; i < n; ++i) {
+        const int vslot = slot == 2 ? 0 : slot + 1;
+        float s[2][4];
+        fetch_wait();
+        held_scores<TIn, D, CACHE>(s, qf, ring[slot], lane);
+        __syncwarp();
+        if (i + 1 < n) fetch<D, true>(ring[slot], vp, c.v_scale, at, lane);
+        fetch_commit();
+        fetch_wait();
+        held_outputs<D, CACHE>(run, s, ring[vslot], lane);
+        __syncwarp();
+        if (i + 2 < n) {
+            at = group_of(i + 2);
+            fetch<D, false>(ring[vslot], kp, c.k_scale, at, lane);
+        }
+        fetch_commit();
+        slot = vslot == 2 ? 0 : vslot + 1;
+    }
 }
 
 // ---- open rows: float32 keys, values in their own type --------------------------------

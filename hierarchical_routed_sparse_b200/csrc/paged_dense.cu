@@ -1,0 +1,312 @@
+// paged_dense.cu -- one query per sequence over the whole of its paged 8-bit
+// cache (no routing): O = softmax(scale q K^T) V over every complete chunk's
+// held values and the open rows 0 .. pos % 64.
+//
+// The sequences of a batch differ in length, and one long sequence may be all
+// there is, so work is cut by keys and not by sequences: the tiles (32 keys)
+// of all units (batch, kv-head) stand in one row, each unit's led by one that
+// stands for its open rows, and every CTA takes the same number of
+// neighbours.  A unit that one CTA holds from end to end is finished there;
+// the parts of the others (output, reference and sum of each head) go to the
+// workspace, and a second kernel joins them.  Which CTA has what follows from
+// the positions, which both kernels read on the device.
+//
+// The kernel streams every code once and is bound by that and, at a few
+// hundred instructions a tile, by instruction issue (paged_attend.cuh).
+#include "paged.cuh"
+#include "paged_attend.cuh"
+#include "sm100.cuh"
+
+namespace hga {
+namespace {
+
+using namespace paged;
+
+constexpr int kWarps = 8, kThreads = 32 * kWarps, kPerSm = 2;
+constexpr int kLeast = 2 * kWarps;                   // tiles of a CTA, where there are few
+constexpr int kPerChunk = kGroupsPerChunk / kTileGroups;
+constexpr int kSitePage = 431, kSiteLength = 432;
+
+struct Args {
+    PagedShape s;
+    hga_paged_cache c;
+    const int32_t* pos;
+    const void* q;
+    float* O;
+    float* lse;
+    float* parts;                                    // [grid][2][G d + 2 G]
+    int grid;                                        // CTAs of the first kernel
+};
+
+// Tiles of a sequence's units: none when it is empty (or its position is
+// past the table: recorded).
+__device__ __forceinline__ int64_t tiles_of(const Args& g, int b)
+{
+    const int64_t p = g.pos[b];
+    if (p < 0) return 0;
+    if (p >= (int64_t)g.s.max_chunks * kChunk) {
+        flag(kSiteLength);
+        return 0;
+    }
+    return 1 + kPerChunk * (p / kChunk);
+}
+
+// What the whole CTA knows of the row of tiles.
+template <int Threads> struct Row {
+    int64_t total;
+    int ctas;                                        // CTAs that get tiles
+    __device__ __forceinline__ int64_t begin(int cta) const { return total * cta / ctas; }
+    __device__ __forceinline__ int cta_of(int64_t tile) const
+    {
+        int i = int(tile * ctas / total);
+        while (begin(i + 1) <= tile) ++i;
+        return i;
+    }
+};
+
+// Sum of `mine` over the CTA, for every thread (synchronises).
+template <int Threads> __device__ __forceinline__ int64_t block_sum(int64_t mine, int64_t* room)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) room[threadIdx.x >> 5] = mine;
+    __syncthreads();
+    int64_t all = 0;
+#pragma unroll
+    for (int w = 0; w < Threads / 32; ++w) all += room[w];
+    return all;
+}
+
+template <int Threads> __device__ __forceinline__ Row<Threads> row_of(const Args& g, int64_t* room)
+{
+    int64_t mine = 0;
+    for (int b = threadIdx.x; b < g.s.B; b += Threads) mine += tiles_of(g, b);
+    Row<Threads> r;
+    r.total = block_sum<Threads>(mine, room) * g.s.Hkv;
+    const int64_t most = (r.total + kLeast - 1) / kLeast;
+    r.ctas = (int)(most < g.grid ? (most > 0 ? most : 1) : g.grid);
+    return r;
+}
+
+// Sequence that holds the tile, and its first unit's first tile.  Every warp
+// looks for itself.
+__device__ __forceinline__ void find(const Args& g, int64_t tile, int& b, int64_t& first)
+{
+    const int lane = threadIdx.x & 31;
+    first = 0;
+    for (int b0 = 0; b0 < g.s.B; b0 += 32) {
+        const int64_t n = b0 + lane < g.s.B ? tiles_of(g, b0 + lane) * g.s.Hkv : 0;
+        int64_t upto = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        const unsigned hit = __ballot_sync(0xFFFFFFFFu, tile < first + upto);
+        if (hit) {
+            const int at = __ffs(hit) - 1;
+            b = b0 + at;
+            first += __shfl_sync(0xFFFFFFFFu, upto - n, at);
+            return;
+        }
+        first += __shfl_sync(0xFFFFFFFFu, upto, 31);
+    }
+    b = g.s.B;
+}
+
+__host__ __device__ inline size_t part_floats(const PagedShape& s) { return (size_t)s.G * s.d + 2 * (size_t)s.G; }
+
+template <int D> constexpr size_t rings_bytes() { return sizeof(Half<D>) * kHalves * kWarps; }
+template <int D> inline size_t dense_smem(const PagedShape& s)
+{
+    const size_t merge = 4 * (size_t)kWarps * s.G * (D + 3);
+    return rings_bytes<D>() > merge ? rings_bytes<D>() : merge;
+}
+
+template <typename TIn, int D, int CACHE>
+__global__ void __launch_bounds__(kThreads, kPerSm) paged_dense_kernel(const __grid_constant__ Args g)
+{
+    extern __shared__ __align__(16) uint8_t sm[];
+    __shared__ int64_t s_room[kWarps];
+    pdl_wait();
+    pdl_trigger();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = g.s.G;
+    const Row<kThreads> row = row_of<kThreads>(g, s_room);
+    if ((int)blockIdx.x >= row.ctas || row.total == 0) return;
+    int64_t at = row.begin(blockIdx.x);
+    const int64_t end = row.begin(blockIdx.x + 1);
+    int b;
+    int64_t first;                                   // of the sequence's first unit
+    find(g, at, b, first);
+
+    while (at < end) {
+        const int64_t n = tiles_of(g, b);
+        if (n == 0 || at >= first + n * g.s.Hkv) {   // to the next sequence
+            first += n * g.s.Hkv;
+            ++b;
+            continue;
+        }
+        const int h = int((at - first) / n);
+        const int64_t unit0 = first + n * h;         // the unit's tiles: unit0 .. unit0 + n - 1
+        const int64_t from = at - unit0, to = end - unit0 < n ? end - unit0 : n;
+        const int64_t bh = (int64_t)b * g.s.Hkv + h, head0 = (int64_t)b * g.s.Hq + h * G;
+        const TIn* q = static_cast<const TIn*>(g.q) + head0 * D;
+        const int32_t* table = g.c.table + (int64_t)b * g.s.max_chunks;
+
+        Running<D> run;
+        run.init();
+        if (from == 0) {                             // the open rows
+            const int rows = int(g.pos[b] % kChunk) + 1;
+            const int64_t r0 = bh * kChunk * D;
+            if (16 * warp < rows)
+                attend_open<TIn, D>(run, q, G, g.c.k_tail + r0, static_cast<const TIn*>(g.c.v_tail) + r0, 16 * warp, rows,
+                                    g.s.scale * kLog2e, lane);
+        }
+        // Tile j > 0 is half (j - 1) % 2 of chunk (j - 1) / 2.  A CTA's last warp
+        // begins, since the first ones have open rows.
+        const int64_t j0 = (from > 0 ? from : 1) - 1 + (kWarps - 1 - warp), j1 = to - 1;
+        const int mine = j1 > j0 ? int((j1 - j0 + kWarps - 1) / kWarps) : 0;
+        int32_t pages = 0;                           // pages of 32 of the warp's tiles, one a lane
+        auto group_of = [&](int i) -> int64_t {
+            if (i % 32 == 0)
+                pages = i + lane < mine
+                            ? (int32_t)page_or_none(__ldg(table + (j0 + (int64_t)(i + lane) * kWarps) / kPerChunk),
+                                                    g.s.n_pages, kSitePage)
+                            : -1;
+            const int32_t page = __shfl_sync(0xFFFFFFFFu, pages, i % 32);
+            const int half = int((j0 + (int64_t)i * kWarps) % kPerChunk);
+            return page < 0 ? -1
+                            : ((int64_t)page * g.s.Hkv + h) * kGroupsPerChunk + kTileGroups * half + lane / 8;
+        };
+        attend_tiles<TIn, D, CACHE>(run, reinterpret_cast<Half<D>*>(sm) + kHalves * warp, mine, group_of, q, G,
+                                    g.s.scale * kLog2e, g.c, lane);
+
+        // The warps' parts meet; f: a warp's factor.
+        __syncthreads();
+        float* om = reinterpret_cast<float*>(sm);    // [kWarps][G][D]
+        float* rm = om + kWarps * G * D;             // [kWarps][G] references, then sums, then factors
+        float* lm = rm + kWarps * G;
+        float* fm = lm + kWarps * G;
+        run.store(om + warp * G * D, rm + warp * G, lm + warp * G, G, lane);
+        __syncthreads();
+        const bool whole = from == 0 && to == n;
+        float* part = g.parts + (2 * (int64_t)blockIdx.x + (from == 0)) * part_floats(g.s);
+        for (int i = tid; i < kWarps * G; i += kThreads) {
+            const int hd = i % G;
+            float M = rm[hd], l = 0.f;
+            for (int w = 1; w < kWarps; ++w) M = fmaxf(M, rm[w * G + hd]);
+            for (int w = 0; w < kWarps; ++w) l = fmaf(lm[w * G + hd], ex2(rm[w * G + hd] - M), l);
+            fm[i] = whole ? ex2(rm[i] - M) / l : ex2(rm[i] - M);
+            if (i < G) {
+                if (whole) {
+                    g.lse[head0 + hd] = (M + log2f(l)) * kLn2;
+                } else {
+                    part[G * D + hd] = M;
+                    part[G * D + G + hd] = l;
+                }
+            }
+        }
+        __syncthreads();
+        float* out = whole ? g.O + head0 * D : part;
+        for (int i = tid; i < G * D; i += kThreads) {
+            float o = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) o = fmaf(om[w * G * D + i], fm[w * G + i / D], o);
+            out[i] = o;
+        }
+        __syncthreads();                             // the rings may be filled again
+        at = unit0 + to;
+    }
+}
+
+// One unit and head a CTA: joins the parts of a unit that several CTAs hold,
+// and writes the outputs of empty sequences.  Lanes of four threads share an
+// element's parts.
+constexpr int kShare = 4;
+template <int D> __global__ void __launch_bounds__(kShare * D) paged_join_kernel(const __grid_constant__ Args g)
+{
+    constexpr int kThreadsJoin = kShare * D;
+    __shared__ int64_t s_room[kThreadsJoin / 32];
+    __shared__ float s_o[kShare][D], s_m[kShare], s_l[kShare];
+    pdl_wait();
+    pdl_trigger();
+    const int tid = threadIdx.x, e = tid % D, lot = tid / D, G = g.s.G;
+    const int64_t bh = blockIdx.x / G;
+    const int hd = blockIdx.x % G, b = int(bh / g.s.Hkv), h = int(bh % g.s.Hkv);
+    const int64_t out = (int64_t)b * g.s.Hq + h * G + hd;
+    int64_t before = 0;
+    for (int i = tid; i < b; i += kThreadsJoin) before += tiles_of(g, i);
+    const Row<kThreadsJoin> row = row_of<kThreadsJoin>(g, s_room);
+    before = block_sum<kThreadsJoin>(before, s_room) * g.s.Hkv;
+    const int64_t n = tiles_of(g, b);
+    if (n == 0) {
+        if (lot == 0) g.O[out * D + e] = 0.f;
+        if (tid == 0) g.lse[out] = -INFINITY;
+        return;
+    }
+    const int64_t unit0 = before + n * h;
+    const int c0 = row.cta_of(unit0), c1 = row.cta_of(unit0 + n - 1);
+    if (c0 == c1) return;                            // one CTA had all of it
+    // CTA c0 holds the unit's first tiles (its second part, or its first when
+    // it begins there), the others begin inside the unit.
+    auto part_of = [&](int c) { return g.parts + (2 * (int64_t)c + (c == c0)) * part_floats(g.s); };
+    float M = -INFINITY, l = 0.f, o = 0.f;
+    for (int c = c0 + lot; c <= c1; c += kShare) M = fmaxf(M, part_of(c)[G * D + hd]);
+#pragma unroll 4
+    for (int c = c0 + lot; c <= c1; c += kShare) {
+        const float* p = part_of(c);
+        const float f = ex2(p[G * D + hd] - M);
+        l = fmaf(p[G * D + G + hd], f, l);
+        o = fmaf(p[hd * D + e], f, o);
+    }
+    s_o[lot][e] = o;
+    if (e == 0) {
+        s_m[lot] = M;
+        s_l[lot] = l;
+    }
+    __syncthreads();
+    if (lot > 0) return;
+    M = s_m[0];
+#pragma unroll
+    for (int i = 1; i < kShare; ++i) M = fmaxf(M, s_m[i]);
+    l = o = 0.f;
+#pragma unroll
+    for (int i = 0; i < kShare; ++i) {
+        const float f = s_m[i] == -INFINITY ? 0.f : ex2(s_m[i] - M);
+        l = fmaf(s_l[i], f, l);
+        o = fmaf(s_o[i][e], f, o);
+    }
+    g.O[out * D + e] = o / l;
+    if (e == 0) g.lse[out] = (M + log2f(l)) * kLn2;
+}
+
+template <typename TIn, int D, int CACHE> cudaError_t launch(const Args& g, cudaStream_t st)
+{
+    auto k = paged_dense_kernel<TIn, D, CACHE>;
+    const size_t smem = dense_smem<D>(g.s);
+    if (cudaError_t e = allow_smem(k, (int)smem)) return e;
+    if (cudaError_t e = launch_pdl(k, dim3((unsigned)g.grid), dim3(kThreads), smem, st, g)) return e;
+    return launch_pdl(paged_join_kernel<D>, dim3((unsigned)(g.s.B * g.s.Hq)), dim3(kShare * D), 0, st, g);
+}
+
+template <typename TIn, int D> cudaError_t by_cache(const Args& g, cudaStream_t st)
+{
+    return g.s.cache_dtype == HGA_INT8 ? launch<TIn, D, HGA_INT8>(g, st) : launch<TIn, D, HGA_E4M3>(g, st);
+}
+
+}  // namespace
+
+size_t paged_dense_workspace(const PagedShape& s) { return sizeof(float) * part_floats(s) * 2 * kPerSm * (size_t)sm_count(); }
+
+cudaError_t launch_paged_dense(const PagedShape& s, const hga_paged_cache& c, const int32_t* pos, const void* q, float* O,
+                               float* lse, void* workspace, cudaStream_t st)
+{
+    const Args g{s, c, pos, q, O, lse, static_cast<float*>(workspace), kPerSm * sm_count()};
+    if (s.dtype == HGA_BF16) return s.d == 128 ? by_cache<__nv_bfloat16, 128>(g, st) : by_cache<__nv_bfloat16, 64>(g, st);
+    return s.d == 128 ? by_cache<float, 128>(g, st) : by_cache<float, 64>(g, st);
+}
+
+HGA_CHECK_WORD_READER(check_word_paged_dense)
+
+}  // namespace hga

@@ -51,16 +51,24 @@ def paged_widths(p: PagedParams) -> tuple[int, int]:
     return wc.value, wg.value
 
 
-def _ints(t, name, *shape):
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
-    return B._here(t, name)
+def paged_workspace_size(p: PagedParams) -> int:
+    """Bytes of device scratch that a dense decode call needs."""
+    return int(B.load().hga_paged_workspace_size(ctypes.byref(p.c())))
+
+
+def _dense(t, name, shape, dtype, dev):
+    """Data pointer of a contiguous tensor on device `dev`, the current one."""
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
+    return B._here(t, name, dev)
 
 
 class PagedCache:
     """The tensors of a paged cache (include/hga.h, hga_paged_cache).  Tensors
     that are not given are allocated: the pool and the open rows zeroed, the
-    table filled with -1 (no page).  Decode calls only read the cache."""
+    table filled with -1 (no page).  Decode calls only read the cache; dense
+    ones share its ``workspace``, so those that may overlap on the GPU are
+    given others."""
 
     def __init__(self, p: PagedParams, device="cuda", **tensors):
         paged_widths(p)                              # the parameters are valid
@@ -81,61 +89,65 @@ class PagedCache:
             if t is None:
                 t = (torch.full(shape, -1, dtype=dtype, device=device) if name == "table"
                      else torch.zeros(shape, dtype=dtype, device=device))
-            elif tuple(t.shape) != shape or t.dtype != dtype or not t.is_contiguous():
+            elif t.shape != shape or t.dtype != dtype or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
             setattr(self, name, t)
             ptrs.append(B._here(t, name))
         self._p, self._c = p.c(), B._PagedCache(*ptrs)
         self._pp, self._pc = ctypes.byref(self._p), ctypes.byref(self._c)
         self._widths = paged_widths(p)
+        n = paged_workspace_size(p)
+        self.workspace = torch.empty(n, dtype=torch.uint8, device=self.table.device) if n else None
+        lib = B.load()
+        self._append, self._decode = lib.hga_paged_append, lib.hga_paged_decode
 
-    def _rows(self, t, name, N, H):
-        if tuple(t.shape) != (N, H, self.p.d) or t.dtype != self.p.torch_dtype or t.stride(2) != 1:
+    def _rows(self, t, name, N, H, dev):
+        if t.shape != (N, H, self.p.d) or t.dtype != self.v_tail.dtype or t.stride(2) != 1:
             raise ValueError(f"{name} must be {self.p.torch_dtype} rows [{N}][{H}][{self.p.d}] with unit stride along d")
-        return B._here(t, name), t.stride(0), t.stride(1)
+        return B._here(t, name, dev), t.stride(0), t.stride(1)
 
     def append(self, pos, k, v, cu=None, q=None, q_out=None, rope=None, interleaved: bool = False, stream=None):
         """Tokens cu[b] .. cu[b + 1] - 1 of k, v [N][Hkv][d] (and q [N][Hq][d])
         join sequence b at positions pos[b], pos[b] + 1, ... (int32, device;
         cu None: one token each).  q_out [N][Hq][d] gets the rotated queries;
         ``rope`` as of ``rope_table`` (None: k and q are taken as they are)."""
-        p = self.p
+        p, dev = self.p, torch.cuda.current_device()
         N = k.shape[0]
-        kr, vr = self._rows(k, "k", N, p.Hkv), self._rows(v, "v", N, p.Hkv)
-        qr, out = (None, 0, 0), None
-        if q is not None:
-            qr = self._rows(q, "q", N, p.Hq)
-        if q_out is not None:
-            out = self._rows(q_out, "q_out", N, p.Hq)[0]
-            if not q_out.is_contiguous():
-                raise ValueError("q_out must be contiguous")
+        kp, kt, kh = self._rows(k, "k", N, p.Hkv, dev)
+        vp, vt, vh = self._rows(v, "v", N, p.Hkv, dev)
+        qp, qt, qh = (None, 0, 0) if q is None else self._rows(q, "q", N, p.Hq, dev)
+        out = None if q_out is None else _dense(q_out, "q_out", (N, p.Hq, p.d), self.v_tail.dtype, dev)
         table, rows, rot = None, 0, 0
         if rope is not None:
             B._check_table(rope, "rope")
-            table = B._here(rope, "rope")
+            table = B._here(rope, "rope", dev)
             rows, rot = rope.shape
-        B._check(B.load().hga_paged_append(
-            self._pp, self._pc, _ints(pos, "pos", p.B), None if cu is None else _ints(cu, "cu", p.B + 1), N, *qr, *kr,
-            *vr, out, table, rows, rot, int(interleaved), B._stream(stream)))
+        code = self._append(
+            self._pp, self._pc, _dense(pos, "pos", (p.B,), torch.int32, dev),
+            None if cu is None else _dense(cu, "cu", (p.B + 1,), torch.int32, dev), N, qp, qt, qh, kp, kt, kh, vp, vt, vh,
+            out, table, rows, rot, interleaved, B._raw_stream(stream, dev))
+        if code:
+            B._check(code)
 
-    def decode(self, pos, q, O, lse, cidx=None, gidx=None, stream=None):
+    def decode(self, pos, q, O, lse, cidx=None, gidx=None, workspace=None, stream=None):
         """The query q [B][Hq][d] of each sequence, at position pos[b] (int32,
         device; negative: empty), attends its cache: O [B][Hq][d] and lse
         [B][Hq] (float32), routing rows cidx [B][Hkv][wc], gidx [B][Hkv][wg]
-        (int32; may be None when k_c = k_g = HGA_ALL)."""
-        p = self.p
+        (int32; may be None when k_c = k_g = HGA_ALL: dense attention, with
+        ``workspace`` of paged_workspace_size bytes, the cache's by default)."""
+        p, dev = self.p, torch.cuda.current_device()
         wc, wg = self._widths
-        if tuple(q.shape) != (p.B, p.Hq, p.d) or q.dtype != p.torch_dtype or not q.is_contiguous():
-            raise ValueError(f"q must be contiguous {p.torch_dtype} [{p.B}][{p.Hq}][{p.d}]")
-        if tuple(O.shape) != (p.B, p.Hq, p.d) or O.dtype != torch.float32 or not O.is_contiguous():
-            raise ValueError(f"O must be contiguous float32 [{p.B}][{p.Hq}][{p.d}]")
-        if tuple(lse.shape) != (p.B, p.Hq) or lse.dtype != torch.float32 or not lse.is_contiguous():
-            raise ValueError(f"lse must be contiguous float32 [{p.B}][{p.Hq}]")
-        B._check(B.load().hga_paged_decode(
-            self._pp, self._pc, _ints(pos, "pos", p.B), B._here(q, "q"), B._here(O, "O"), B._here(lse, "lse"),
-            None if cidx is None else _ints(cidx, "cidx", p.B, p.Hkv, wc),
-            None if gidx is None else _ints(gidx, "gidx", p.B, p.Hkv, wg),
-            B._stream(stream)))
+        ws = self.workspace if workspace is None else workspace
+        code = self._decode(
+            self._pp, self._pc, _dense(pos, "pos", (p.B,), torch.int32, dev),
+            _dense(q, "q", (p.B, p.Hq, p.d), self.v_tail.dtype, dev),
+            _dense(O, "O", (p.B, p.Hq, p.d), torch.float32, dev), _dense(lse, "lse", (p.B, p.Hq), torch.float32, dev),
+            None if cidx is None else _dense(cidx, "cidx", (p.B, p.Hkv, wc), torch.int32, dev),
+            None if gidx is None else _dense(gidx, "gidx", (p.B, p.Hkv, wg), torch.int32, dev),
+            None if ws is None else B._here(ws, "workspace", dev), 0 if ws is None else ws.numel() * ws.element_size(),
+            B._raw_stream(stream, dev))
+        if code:
+            B._check(code)
 
 
 class PagedDecodeState:

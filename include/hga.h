@@ -432,6 +432,11 @@ int hga_paged_append(const hga_paged_params* p, const hga_paged_cache* c, const 
  * (8 * wc for HGA_ALL). */
 int hga_paged_widths(const hga_paged_params* p, int* wc, int* wg);
 
+/* Bytes of device scratch that hga_paged_decode needs on the current device
+ * for dense attention (k_c = k_g = HGA_ALL); 0 when routed, or on invalid
+ * parameters. */
+size_t hga_paged_workspace_size(const hga_paged_params* p);
+
 /* One decode step: the query of sequence b stands at position pos[b], in the
  * chunk of the last token that hga_paged_append has put into the cache
  * (pos[b] is that token's position in a generation step; negative: an empty
@@ -445,10 +450,14 @@ int hga_paged_widths(const hga_paged_params* p, int* wc, int* wg);
  *   O     [B][Hq][d] float32;  lse [B][Hq] float32, natural log
  *   cidx  [B][Hkv][wc], gidx [B][Hkv][wg] int32 (hga_paged_widths), written;
  *         both may be NULL when k_c = k_g = HGA_ALL
+ *   workspace  16-byte aligned, ws_bytes >= hga_paged_workspace_size(p); used
+ *         (and checked) when cidx and gidx are NULL.  Calls that may overlap
+ *         on the GPU need workspaces of their own.
  * At most 8 q-heads per kv-head; HGA_ERR_UNSUPPORTED too when the routing
  * state of max_chunks and k_c exceeds shared memory. */
 int hga_paged_decode(const hga_paged_params* p, const hga_paged_cache* c, const int32_t* pos, const void* q,
-                     float* O, float* lse, int32_t* cidx, int32_t* gidx, hga_stream_t stream);
+                     float* O, float* lse, int32_t* cidx, int32_t* gidx, void* workspace, size_t ws_bytes,
+                     hga_stream_t stream);
 
 /* Status word of the kernels' bounded waits: every wait of a tensor-core
  * kernel or of the decode kernel on a barrier gives up after one second, records the code of the wait

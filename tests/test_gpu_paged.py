@@ -475,7 +475,7 @@ def test_bad_pages_and_positions_are_left_out():
     keep = c.table.clone()
     c.table[0, 2] = 20
     O, lse, _, _ = _decode(c, [383, 384], q, rows=False)
-    assert hga.device_check(clear=True) in (421, 422)
+    assert hga.device_check(clear=True) in (431, 432)
     assert (O[1] == 0).all() and np.isneginf(lse[1]).all()
     # what is left: chunks 0, 1, 3, 4 and the open rows
     k2 = _params(1, 4, 1, 128, 20, 5, "bf16", "int8")
@@ -523,11 +523,12 @@ def test_offsets_past_32_bits():
 
 
 def test_two_streams_and_two_graphs_at_once():
-    # Calls that overlap read one cache.
+    # Calls that overlap: one cache, workspaces of their own.
     p = _params(4, 8, 2, 128, 200, 40, "bf16", "int8")
     c, q = _filled(p, "int8", [2500, 1700, 64, 0])
     pos = _int32([2499, 1699, 63, -1])
     want = _decode(c, [2499, 1699, 63, -1], q, rows=False)
+    ws = [torch.empty(hga.paged_workspace_size(p), dtype=torch.uint8, device="cuda") for _ in range(2)]
     O = [torch.empty(4, 8, 128, device="cuda") for _ in range(2)]
     lse = [torch.empty(4, 8, device="cuda") for _ in range(2)]
     streams = [torch.cuda.Stream() for _ in range(2)]
@@ -535,10 +536,10 @@ def test_two_streams_and_two_graphs_at_once():
     for i, s in enumerate(streams):
         s.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(s):
-            c.decode(pos, q, O[i], lse[i])
+            c.decode(pos, q, O[i], lse[i], workspace=ws[i])
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g, stream=s):
-            c.decode(pos, q, O[i], lse[i])
+            c.decode(pos, q, O[i], lse[i], workspace=ws[i])
         graphs.append(g)
     torch.cuda.synchronize()
     for _ in range(20):

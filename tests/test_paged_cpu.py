@@ -40,7 +40,7 @@ def test_paged_params_are_refused(lib, kw, code):
     assert lib.hga_paged_widths(ctypes.byref(p), ctypes.byref(wc), ctypes.byref(wg)) == code
     assert lib.hga_last_error().decode()
     c = B._PagedCache(*[16] * 9)
-    assert lib.hga_paged_decode(ctypes.byref(p), ctypes.byref(c), P16, P16, P16, P16, P16, P16, None) == code
+    assert lib.hga_paged_decode(ctypes.byref(p), ctypes.byref(c), P16, P16, P16, P16, P16, P16, P16, 1 << 40, None) == code
     assert _append(lib, p, c) == code
 
 
@@ -77,7 +77,7 @@ def test_cache_pointers_are_checked(lib, i):
         ptr[i] = bad
         c, p = B._PagedCache(*ptr), _paged().c()
         assert _append(lib, p, c) == BAD
-        assert lib.hga_paged_decode(ctypes.byref(p), ctypes.byref(c), P16, P16, P16, P16, P16, P16, None) == BAD
+        assert lib.hga_paged_decode(ctypes.byref(p), ctypes.byref(c), P16, P16, P16, P16, P16, P16, P16, 1 << 40, None) == BAD
 
 
 def test_append_of_nothing_is_a_no_op(lib):
@@ -87,13 +87,19 @@ def test_append_of_nothing_is_a_no_op(lib):
 def test_decode_refusals(lib):
     c = B._PagedCache(*[16] * 9)
 
-    def call(p, pos=P16, q=P16, O=P16, lse=P16, cidx=P16, gidx=P16):
-        return lib.hga_paged_decode(ctypes.byref(p.c()), ctypes.byref(c), pos, q, O, lse, cidx, gidx, None)
+    def call(p, pos=P16, q=P16, O=P16, lse=P16, cidx=P16, gidx=P16, ws=P16, n=1 << 40):
+        return lib.hga_paged_decode(ctypes.byref(p.c()), ctypes.byref(c), pos, q, O, lse, cidx, gidx, ws, n, None)
 
     for name in ("pos", "q", "O", "lse", "cidx", "gidx"):
         assert call(_paged(), **{name: None}) == BAD, name
     assert call(_paged(k_c=hga.HGA_ALL, k_g=hga.HGA_ALL), cidx=None) == BAD       # one without the other
     assert call(_paged(k_c=hga.HGA_ALL), cidx=None, gidx=None) == BAD
+    dense = _paged(k_c=hga.HGA_ALL, k_g=hga.HGA_ALL)
+    need = hga.paged_workspace_size(dense)
+    assert need > 0 and hga.paged_workspace_size(_paged()) == 0
+    assert call(dense, cidx=None, gidx=None, n=need - 1) == BAD
+    assert call(dense, cidx=None, gidx=None, ws=None) == BAD
+    assert call(dense, cidx=None, gidx=None, ws=ctypes.c_void_p(4)) == BAD
     assert call(_paged(Hq=18, Hkv=2)) == UNSUP                                    # 9 q-heads per kv-head
     assert call(_paged(k_c=1 << 14, max_chunks=1 << 14)) == UNSUP                 # routing state past shared memory
 
