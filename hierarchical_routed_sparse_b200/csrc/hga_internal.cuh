@@ -165,10 +165,6 @@ cudaError_t allow_smem(Kern kernel, int bytes)
     return allow_smem_fn(reinterpret_cast<const void*>(kernel), bytes);
 }
 
-// Let a kernel be launched with clusters of more than 8 CTAs (once per kernel
-// and device; tma_map.cu).
-cudaError_t allow_large_clusters(const void* kernel);
-
 // ---- launchers (each returns cudaError_t of its launch) ------------------------
 // K holds T_src rows per (batch, kv-head), the first of them at position row0.
 cudaError_t launch_summaries(const Shape& s, const void* K, int64_t T_src, int64_t row0, int64_t c_begin,

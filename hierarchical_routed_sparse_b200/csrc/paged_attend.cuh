@@ -33,11 +33,11 @@
 //
 // Running softmax, in units of log2.  With s the score and v the group's value
 // scale, a weight enters the products as e v, e = 2^(s - R).  The reference R
-// follows the largest s + log2 v, so that e v stays below 2^15 whatever the
-// scales are, and it moves only when that would be exceeded: R is
-// 12 below the maximum it was set from, so most tiles find it as it should
-// be and weights down to 2^-24 of the largest keep all their bits.  (Open
-// rows take the largest of their values for v, for the reference alone.)
+// follows a tile's largest s + log2 of its largest v, so that e v stays below
+// 2^15 whatever the scales are, and it moves only when that would be exceeded:
+// R is 12 below the maximum it was set from, so most tiles find it as it
+// should be and weights down to 2^-24 of the largest keep all their bits.
+// (Open rows take the largest of their values for v, for the reference alone.)
 // The normalising sum collects e, which stays below 2^105 since log2 v counts
 // as at least -90 there; values below 2^-90 lose bits.
 #pragma once
@@ -76,6 +76,14 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same from a zero sum.
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 // Transpose of an 8 x 8 matrix of 16-bit elements, two of a row in each lane.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x)
@@ -273,7 +281,7 @@ constexpr int kTileGroups = 4, kTileKeys = kTileGroups * kGroup;
 constexpr int kHalves = 3;                           // halves in a warp's ring
 template <int D> struct alignas(16) Half {
     uint8_t code[kTileKeys * D];
-    float scale[kTileGroups];
+    alignas(16) float scale[kTileGroups];
 };
 
 // 16-byte pieces of a row change places: K by the row's parity (eight lanes
@@ -285,10 +293,11 @@ template <int D, bool V> __device__ __forceinline__ int piece(int row, int c)
     return D == 128 ? c ^ (4 * (row & 1)) : c;
 }
 
-__device__ __forceinline__ void cp16(void* dst, const void* src, bool there)
+// 16 bytes from src + kFrom to dst + kTo of shared memory; bytes = 0 fills zeros.
+template <int kTo, int kFrom> __device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
-                 "r"(there ? 16 : 0)
+    asm volatile("cp.async.cg.shared.global [%0+%3], [%1+%4], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes), "n"(kTo),
+                 "n"(kFrom)
                  : "memory");
 }
 
@@ -297,14 +306,30 @@ __device__ __forceinline__ void cp16(void* dst, const void* src, bool there)
 template <int D, bool V>
 __device__ __forceinline__ void fetch(Half<D>& s, const uint8_t* codes, const float* scales, int64_t at, int lane)
 {
-    constexpr int kPieces = D / 16, kRows = 8 / kPieces;         // pieces of a row; rows that 8 lanes copy at once
     const int x = lane >> 3, c = lane & 7;
     const bool there = at >= 0;
+    const int bytes = there ? 16 : 0;
     const uint8_t* from = codes + (there ? at : 0) * (kGroup * D) + 16 * c;
-#pragma unroll
-    for (int m = 0; m < kGroup / kRows; ++m) {
-        const int row = kRows * m + c / kPieces;
-        cp16(s.code + (kGroup * x + row) * D + 16 * piece<D, V>(row, c % kPieces), from + m * 128, there);
+    const uint32_t to = (uint32_t)__cvta_generic_to_shared(s.code) + x * (kGroup * D);
+    if constexpr (D == 128) {                        // a row at a time, its piece c
+        const uint32_t even = to + 16 * c;
+        const uint32_t r2 = to + 16 * (V ? c ^ 2 : c), r4 = to + 16 * (V ? c ^ 4 : c), r6 = to + 16 * (V ? c ^ 6 : c);
+        const uint32_t odd = V ? even : to + 16 * (c ^ 4);       // piece<D, V>(row, c)
+        cp16<0, 0>(even, from, bytes);
+        cp16<128, 128>(odd, from, bytes);
+        cp16<256, 256>(r2, from, bytes);
+        cp16<384, 384>(V ? r2 : odd, from, bytes);
+        cp16<512, 512>(r4, from, bytes);
+        cp16<640, 640>(V ? r4 : odd, from, bytes);
+        cp16<768, 768>(r6, from, bytes);
+        cp16<896, 896>(V ? r6 : odd, from, bytes);
+    } else {                                         // two rows at a time
+        const uint32_t at0 = to + 64 * (c >> 2);
+        const int p = c & 3;
+        cp16<0, 0>(at0 + 16 * p, from, bytes);
+        cp16<128, 128>(at0 + 16 * (V ? p ^ 1 : p), from, bytes);
+        cp16<256, 256>(at0 + 16 * (V ? p ^ 2 : p), from, bytes);
+        cp16<384, 384>(at0 + 16 * (V ? p ^ 3 : p), from, bytes);
     }
     if (c == 0) {
         if (there)
@@ -340,10 +365,6 @@ __device__ __forceinline__ void held_scores(float (&s)[2][4], const Query<TIn, D
     const int g = lane >> 2, t = lane & 3;
     float r[2][4];                                   // two chains of products for each half of the tile
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[x][e] = r[x][e] = 0.f;
-#pragma unroll
     for (int j = 0; j < D / 64; ++j)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -354,22 +375,21 @@ __device__ __forceinline__ void held_scores(float (&s)[2][4], const Query<TIn, D
             for (int i = 0; i < 4; ++i) {
                 const uint32_t ua = C::prep(wa[i]), uz = C::prep(wz[i]);
                 const uint32_t a0 = C::low(ua), a1 = C::low(uz), a2 = C::high(ua), a3 = C::high(uz);
-                mma_f16(i & 1 ? r[x] : s[x], a0, a1, a2, a3, q.b[4 * j + i][0], q.b[4 * j + i][1]);
+                const uint32_t b0 = q.b[4 * j + i][0], b1 = q.b[4 * j + i][1];
+                if (j == 0 && i < 2) mma_f16_first(i ? r[x] : s[x], a0, a1, a2, a3, b0, b1);
+                else mma_f16(i & 1 ? r[x] : s[x], a0, a1, a2, a3, b0, b1);
                 if constexpr (Query<TIn, D>::kTwo)
-                    mma_f16(i & 1 ? s[x] : r[x], a0, a1, a2, a3, q.c[4 * j + i][0], q.c[4 * j + i][1]);
+                    mma_f16(i & 1 ? r[x] : s[x], a0, a1, a2, a3, q.c[4 * j + i][0], q.c[4 * j + i][1]);
             }
         }
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            const float ks = k.scale[2 * x + y];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                s[x][2 * y + e] = (s[x][2 * y + e] + r[x][2 * y + e]) * ((e ? q.f1 : q.f0) * ks);
-                if (ks < 0.f) s[x][2 * y + e] = -INFINITY;       // (a NaN scale is there)
-            }
-        }
+    for (int y = 0; y < 4; ++y) {
+        const float ks = k.scale[y], none = ks < 0.f ? -INFINITY : 0.f;      // (a NaN scale is there)
+        const float f0 = q.f0 * ks, f1 = q.f1 * ks;
+        float* v = s[y / 2] + 2 * (y % 2);
+        v[0] = fmaf(v[0] + r[y / 2][2 * (y % 2)], f0, none);
+        v[1] = fmaf(v[1] + r[y / 2][2 * (y % 2) + 1], f1, none);
+    }
 }
 
 // The tile's weights and outputs, given its scores.
@@ -378,15 +398,12 @@ __device__ __forceinline__ void held_outputs(Running<D>& run, const float (&s)[2
 {
     using C = Codes<CACHE>;
     const int g = lane >> 2, t = lane & 3;
-    float vs[4], m0 = -INFINITY, m1 = -INFINITY;
-#pragma unroll
-    for (int y = 0; y < 4; ++y) {
-        vs[y] = v.scale[y];
-        const float lv = log2_above(vs[y]);
-        m0 = fmaxf(m0, s[y / 2][2 * (y % 2)] + lv);
-        m1 = fmaxf(m1, s[y / 2][2 * (y % 2) + 1] + lv);
-    }
-    run.follow(m0, m1);
+    const float4 scales = *reinterpret_cast<const float4*>(v.scale);
+    const float vs[4] = {scales.x, scales.y, scales.z, scales.w};
+    // (fmaxf passes a NaN scale over.)
+    const float lv = log2_above(fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3])));
+    run.follow(fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2])) + lv,
+               fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3])) + lv);
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int y = 0; y < 4; ++y) {
@@ -415,9 +432,9 @@ __device__ __forceinline__ void held_outputs(Running<D>& run, const float (&s)[2
                 a[x][2] = C::low(w[2 * x + 1]);
                 a[x][3] = C::high(w[2 * x + 1]);
             }
-            float o[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int x = 0; x < 2; ++x) mma_f16(o, a[x][0], a[x][1], a[x][2], a[x][3], lo[2 * x], lo[2 * x + 1]);
+            float o[4];
+            mma_f16_first(o, a[0][0], a[0][1], a[0][2], a[0][3], lo[0], lo[1]);
+            mma_f16(o, a[1][0], a[1][1], a[1][2], a[1][3], lo[2], lo[3]);
 #pragma unroll
             for (int x = 0; x < 2; ++x) mma_f16(o, a[x][0], a[x][1], a[x][2], a[x][3], hi[2 * x], hi[2 * x + 1]);
 #pragma unroll
@@ -494,9 +511,24 @@ __device__ __forceinline__ void attend_tiles(Running<D>& run, Half<D>* ring, int
 }
 
 // ---- open rows: float32 keys, values in their own type --------------------------------
-// A float32 is exactly the sum of three bfloat16 (its bits 8 and 8 and 8), so
-// products of such parts lose nothing but the terms below 2^-24 that are left
-// out.
+// Scores by tf32 products (m16n8k8): a float32 is the sum of two tf32 parts,
+// 11 bits and 11 of the other 13, a bfloat16 is one.  Weights times values by
+// bfloat16 products: a float32 is exactly the sum of three bfloat16 (its bits
+// 8 and 8 and 8).  Products of parts below 2^-22 and 2^-24 of the whole are
+// left out.
+__device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo)
+{
+    hi = __float_as_uint(x) & 0xFFFFE000u;
+    lo = __float_as_uint(x - __uint_as_float(hi));
+}
 
 // The upper halves of two words, the first in the low half.
 __device__ __forceinline__ uint32_t upper(float x0, float x1) { return __byte_perm(__float_as_uint(x0), __float_as_uint(x1), 0x7632); }
@@ -506,19 +538,40 @@ __device__ __forceinline__ void split3(float x0, float x1, uint32_t (&p)[3])
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
         p[i] = upper(x0, x1);
+        if (i == 2) break;
         x0 -= __uint_as_float(p[i] << 16);
         x1 -= __uint_as_float(p[i] & 0xFFFF0000u);
     }
 }
 
-// Parts i of one operand and j of the other: the smallest products first.
-template <int NA, int NB, typename F> __device__ __forceinline__ void each_product(F f)
+// log2_above of the largest value of rows row0 .. row0 + 15 (two lanes a row).
+template <typename TIn, int D> __device__ __forceinline__ float open_log2(const TIn* v, int row0, int rows, int lane)
 {
+    const int row = row0 + lane / 2;
+    float top = 0.f;
+    if (row < rows) {
+        const uint4* p = reinterpret_cast<const uint4*>(v + row * D + (lane & 1) * (D / 2));
+        constexpr int N = D / 2 * (int)sizeof(TIn) / 16;
+        if constexpr (sizeof(TIn) == 2) {
+            __nv_bfloat162 m = __float2bfloat162_rn(0.f);
 #pragma unroll
-    for (int n = 2; n >= 0; --n)
+            for (int i = 0; i < N; ++i) {
+                const uint4 w = __ldg(p + i);
+                const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int i = n; i >= 0; --i)
-            if (i < NA && n - i < NB) f(i, n - i);
+                for (int e = 0; e < 4; ++e) m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(x + e)));
+            }
+            top = fmaxf(__low2float(m), __high2float(m));
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint4 w = __ldg(p + i);
+                top = fmaxf(fmaxf(fmaxf(top, fabsf(__uint_as_float(w.x))), fabsf(__uint_as_float(w.y))),
+                            fmaxf(fabsf(__uint_as_float(w.z)), fabsf(__uint_as_float(w.w))));
+            }
+        }
+    }
+    return log2_above(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top))));
 }
 
 // Keys row0 .. row0 + 15 of the open rows (those below `rows`).
@@ -526,50 +579,46 @@ template <typename TIn, int D>
 __device__ __forceinline__ void attend_open(Running<D>& run, const TIn* q, int G, const float* k, const TIn* v, int row0,
                                             int rows, float scale, int lane)
 {
-    constexpr int N = sizeof(TIn) == 4 ? 3 : 1;      // parts of q and of v
+    constexpr bool kF32 = sizeof(TIn) == 4;
     const int g = lane >> 2, t = lane & 3;
     const int ra = row0 + g, rz = row0 + 8 + g;
     const bool ha = ra < rows, hz = rz < rows;
     const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-        const int d = 64 * (i / 4) + 16 * t + 4 * (i % 4);
+    float s[4] = {0.f, 0.f, 0.f, 0.f}, r[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int i = 0; i < D / 16; ++i) {               // d = 16 i + 4 t .. + 3: two products of 8
+        const int d = 16 * i + 4 * t;
         const float4 xa = ha ? __ldg(reinterpret_cast<const float4*>(k + ra * D + d)) : none;
         const float4 xz = hz ? __ldg(reinterpret_cast<const float4*>(k + rz * D + d)) : none;
-        uint32_t a0[3], a1[3], a2[3], a3[3], b0[3], b1[3];
-        split3(xa.x, xa.y, a0);
-        split3(xz.x, xz.y, a1);
-        split3(xa.z, xa.w, a2);
-        split3(xz.z, xz.w, a3);
-        if constexpr (N == 1) {
-            const uint2 w = g < G ? __ldg(reinterpret_cast<const uint2*>(q + g * D + d)) : make_uint2(0u, 0u);
-            b0[0] = w.x;
-            b1[0] = w.y;
-        } else {
-            const float4 w = g < G ? __ldg(reinterpret_cast<const float4*>(q + g * D + d)) : none;
-            split3(w.x, w.y, b0);
-            split3(w.z, w.w, b1);
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
+        if (g < G) load4(q + g * D + d, y);
+        uint32_t h[8], l[8];
+        split_tf32(xa.x, h[0], l[0]);
+        split_tf32(xz.x, h[1], l[1]);
+        split_tf32(xa.y, h[2], l[2]);
+        split_tf32(xz.y, h[3], l[3]);
+        split_tf32(xa.z, h[4], l[4]);
+        split_tf32(xz.z, h[5], l[5]);
+        split_tf32(xa.w, h[6], l[6]);
+        split_tf32(xz.w, h[7], l[7]);
+        uint32_t b[4], c[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (kF32) split_tf32(y[e], b[e], c[e]);
+            else b[e] = __float_as_uint(y[e]);
         }
-        each_product<3, N>([&](int x, int y) { mma_bf16(s, a0[x], a1[x], a2[x], a3[x], b0[y], b1[y]); });
+        mma_tf32(r, l[0], l[1], l[2], l[3], b[0], b[1]);
+        mma_tf32(r, l[4], l[5], l[6], l[7], b[2], b[3]);
+        if constexpr (kF32) {
+            mma_tf32(r, h[0], h[1], h[2], h[3], c[0], c[1]);
+            mma_tf32(r, h[4], h[5], h[6], h[7], c[2], c[3]);
+        }
+        mma_tf32(s, h[0], h[1], h[2], h[3], b[0], b[1]);
+        mma_tf32(s, h[4], h[5], h[6], h[7], b[2], b[3]);
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s[e] = (e < 2 ? ha : hz) ? s[e] * scale : -INFINITY;
-    uint32_t top = 0;                                // largest value of the tile: two lanes a row, 16 bytes at a time
-    if (const int row = row0 + lane / 2; row < rows) {
-        constexpr int kEach = 16 / sizeof(TIn);
-#pragma unroll
-        for (int d = 0; d < D / 2; d += kEach) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(v + row * D + (lane & 1) * (D / 2) + d));
-            const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                top = max(top, x[i] & (sizeof(TIn) == 4 ? 0x7FFFFFFFu : 0x7FFF0000u));
-                if (sizeof(TIn) == 2) top = max(top, (x[i] & 0x7FFFu) << 16);
-            }
-        }
-    }
-    const float lv = log2_above(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, top)));
+    for (int e = 0; e < 4; ++e) s[e] = (e < 2 ? ha : hz) ? (s[e] + r[e]) * scale : -INFINITY;
+    const float lv = open_log2<TIn, D>(v, row0, rows, lane);
     run.follow(fmaxf(s[0], s[2]) + lv, fmaxf(s[1], s[3]) + lv);
     const float e0 = ex2(s[0] - run.R0), e1 = ex2(s[1] - run.R1), e2 = ex2(s[2] - run.R0), e3 = ex2(s[3] - run.R1);
     run.l0 += e0 + e2;
@@ -584,15 +633,15 @@ __device__ __forceinline__ void attend_open(Running<D>& run, const TIn* q, int G
     }
     // Rows 2t, 2t + 1 and 8 + 2t, 8 + 2t + 1; a row that is not there counts as zero.
     const int r0 = row0 + 2 * t;
-    const int r[4] = {r0, r0 + 1, r0 + 8, r0 + 9};
+    const int row[4] = {r0, r0 + 1, r0 + 8, r0 + 9};
 #pragma unroll
     for (int i = 0; i < D / 16; i += 2) {            // d = (D/8) g + 2i .. + 3
         const int d = (D / 8) * g + 2 * i;
-        if constexpr (N == 1) {
+        if constexpr (!kF32) {
             uint2 w[4];
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-                w[x] = r[x] < rows ? __ldg(reinterpret_cast<const uint2*>(v + r[x] * D + d)) : make_uint2(0u, 0u);
+                w[x] = row[x] < rows ? __ldg(reinterpret_cast<const uint2*>(v + row[x] * D + d)) : make_uint2(0u, 0u);
 #pragma unroll
             for (int x = 2; x >= 0; --x) {
                 mma_bf16(run.acc[i], __byte_perm(w[0].x, w[1].x, 0x5410), __byte_perm(w[0].x, w[1].x, 0x7632),
@@ -603,7 +652,7 @@ __device__ __forceinline__ void attend_open(Running<D>& run, const TIn* q, int G
         } else {
             float4 w[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) w[x] = r[x] < rows ? __ldg(reinterpret_cast<const float4*>(v + r[x] * D + d)) : none;
+            for (int x = 0; x < 4; ++x) w[x] = row[x] < rows ? __ldg(reinterpret_cast<const float4*>(v + row[x] * D + d)) : none;
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
                 uint32_t a0[3], a1[3], a2[3], a3[3];
@@ -611,7 +660,10 @@ __device__ __forceinline__ void attend_open(Running<D>& run, const TIn* q, int G
                 split3(m ? w[0].w : w[0].y, m ? w[1].w : w[1].y, a1);
                 split3(m ? w[2].z : w[2].x, m ? w[3].z : w[3].x, a2);
                 split3(m ? w[2].w : w[2].y, m ? w[3].w : w[3].y, a3);
-                each_product<3, 3>([&](int x, int y) { mma_bf16(run.acc[i + m], a0[x], a1[x], a2[x], a3[x], w0[y], w1[y]); });
+#pragma unroll
+                for (int n = 2; n >= 0; --n)         // parts x of V and n - x of the weights, the smallest first
+#pragma unroll
+                    for (int x = 0; x <= n; ++x) mma_bf16(run.acc[i + m], a0[x], a1[x], a2[x], a3[x], w0[n - x], w1[n - x]);
             }
         }
     }

@@ -36,7 +36,7 @@ using sm100::peer_addr;
 using sm100::smem_u32;
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr int kMaxS = 16;                            // CTAs per (batch, kv-head)
+constexpr int kMaxS = 8;                             // CTAs per (batch, kv-head)
 constexpr int kSitePage = 421, kSiteLength = 422;
 
 struct Args {
@@ -375,8 +375,6 @@ cudaError_t launch(const Args& g, cudaStream_t st)
     const size_t smem = layout<D>(g.s, g.S).total;
     auto k = paged_decode_kernel<TIn, D, CACHE>;
     if (cudaError_t e = allow_smem(k, (int)smem)) return e;
-    if (g.S > 8)
-        if (cudaError_t e = allow_large_clusters(reinterpret_cast<const void*>(k))) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(g.s.B * g.s.Hkv * g.S));
     cfg.blockDim = dim3(kThreads);
@@ -400,14 +398,18 @@ cudaError_t by_cache(const Args& g, cudaStream_t st)
     return g.s.cache_dtype == HGA_INT8 ? launch<TIn, D, HGA_INT8>(g, st) : launch<TIn, D, HGA_E4M3>(g, st);
 }
 
-// CTAs per (batch, kv-head): a power of two, as many as keep the grid within
-// what the GPU holds at once, and no more than there are chunks to share.
+// CTAs per (batch, kv-head), a power of two.  Measured at 16K context, k_c 8,
+// k_g 32 (us a call with 1, 2, 4, 8, 16 CTAs): 8 units 22.3, 18.2, 15.9, 15.3,
+// 16.5; 64 units 22.9, 18.7, 18.0, 20.7, 39.3; 128 units 26.2, 23.2, 23.7,
+// 42.9; 256 units 35.9, 30.5, 48.8; 512 units 42.9, 57.8.  So: two where the
+// GPU holds them all at once, more where it holds them at two a SM, or at
+// four when there are many chunks to score (64K context, 128 units: 82, 57,
+// 44, 77), and no more than chunks to share.
 int split(const PagedShape& s)
 {
-    const int most = layout<128>(s, kMaxS).total <= 100 * 1024 ? kMaxS : 8;   // 16 CTAs must fit one GPC's SMs
-    const int64_t units = (int64_t)s.B * s.Hkv, room = 4 * (int64_t)sm_count();
+    const int64_t units = (int64_t)s.B * s.Hkv, sms = sm_count();
     int S = 1;
-    while (S < most && units * S * 2 <= room && S * 4 <= s.max_chunks) S *= 2;
+    while (S < kMaxS && S * 4 <= s.max_chunks && units * S * 2 <= (S == 1 || s.max_chunks >= 1024 ? 4 : 2) * sms) S *= 2;
     return S;
 }
 

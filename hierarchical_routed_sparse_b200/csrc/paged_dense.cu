@@ -168,16 +168,17 @@ __global__ void __launch_bounds__(kThreads, kPerSm) paged_dense_kernel(const __g
         const int64_t j0 = (from > 0 ? from : 1) - 1 + (kWarps - 1 - warp), j1 = to - 1;
         const int mine = j1 > j0 ? int((j1 - j0 + kWarps - 1) / kWarps) : 0;
         int32_t pages = 0;                           // pages of 32 of the warp's tiles, one a lane
+        static_assert(kWarps % kPerChunk == 0, "a warp's tiles are the same part of their chunks");
+        const int64_t chunk0 = j0 / kPerChunk;
+        const int in_page = h * kGroupsPerChunk + kTileGroups * int(j0 % kPerChunk) + lane / 8;
+        const int page_groups = g.s.Hkv * kGroupsPerChunk;
         auto group_of = [&](int i) -> int64_t {
             if (i % 32 == 0)
-                pages = i + lane < mine
-                            ? (int32_t)page_or_none(__ldg(table + (j0 + (int64_t)(i + lane) * kWarps) / kPerChunk),
-                                                    g.s.n_pages, kSitePage)
-                            : -1;
+                pages = i + lane < mine ? (int32_t)page_or_none(__ldg(table + chunk0 + (i + lane) * (kWarps / kPerChunk)),
+                                                                g.s.n_pages, kSitePage)
+                                        : -1;
             const int32_t page = __shfl_sync(0xFFFFFFFFu, pages, i % 32);
-            const int half = int((j0 + (int64_t)i * kWarps) % kPerChunk);
-            return page < 0 ? -1
-                            : ((int64_t)page * g.s.Hkv + h) * kGroupsPerChunk + kTileGroups * half + lane / 8;
+            return page < 0 ? -1 : (int64_t)page * page_groups + in_page;
         };
         attend_tiles<TIn, D, CACHE>(run, reinterpret_cast<Half<D>*>(sm) + kHalves * warp, mine, group_of, q, G,
                                     g.s.scale * kLog2e, g.c, lane);

@@ -54,26 +54,6 @@ cudaError_t allow_smem_fn(const void* kernel, int bytes)
     return e;
 }
 
-cudaError_t allow_large_clusters(const void* kernel)
-{
-    struct Entry {
-        const void* fn;
-        int dev;
-    };
-    static std::mutex mu;
-    static Entry done[256];                          // full: the attribute is set again on every call
-    static int n = 0;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    std::lock_guard<std::mutex> lock(mu);
-    for (int i = 0; i < n; ++i)
-        if (done[i].fn == kernel && done[i].dev == dev) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess && n < 256) done[n++] = Entry{kernel, dev};
-    return e;
-}
-
 int sm_count()
 {
     static int cached[64] = {};
