@@ -222,17 +222,17 @@ __global__ void __launch_bounds__(kThreads, kPerSm) paged_dense_kernel(const __g
 }
 
 // One unit and head a CTA: joins the parts of a unit that several CTAs hold,
-// and writes the outputs of empty sequences.  Lanes of four threads share an
-// element's parts.
-constexpr int kShare = 4;
+// and writes the outputs of empty sequences.  kShare threads share an
+// element's parts.  Until pdl_wait only the caller's inputs are read: the
+// first kernel's CTAs let this one start after their own wait, when whatever
+// wrote the inputs is done.
+constexpr int kShare = 4, kParts = 256;              // parts whose factors are formed at once
 template <int D> __global__ void __launch_bounds__(kShare * D) paged_join_kernel(const __grid_constant__ Args g)
 {
     constexpr int kThreadsJoin = kShare * D;
     __shared__ int64_t s_room[kThreadsJoin / 32];
-    __shared__ float s_o[kShare][D], s_m[kShare], s_l[kShare];
-    pdl_wait();
-    pdl_trigger();
-    const int tid = threadIdx.x, e = tid % D, lot = tid / D, G = g.s.G;
+    __shared__ float s_o[kShare][D], s_f[kParts], s_red[kThreadsJoin / 32];
+    const int tid = threadIdx.x, e = tid % D, lot = tid / D, lane = tid & 31, G = g.s.G;
     const int64_t bh = blockIdx.x / G;
     const int hd = blockIdx.x % G, b = int(bh / g.s.Hkv), h = int(bh % g.s.Hkv);
     const int64_t out = (int64_t)b * g.s.Hq + h * G + hd;
@@ -241,43 +241,56 @@ template <int D> __global__ void __launch_bounds__(kShare * D) paged_join_kernel
     const Row<kThreadsJoin> row = row_of<kThreadsJoin>(g, s_room);
     before = block_sum<kThreadsJoin>(before, s_room) * g.s.Hkv;
     const int64_t n = tiles_of(g, b);
+    const int64_t unit0 = before + n * h;
+    const int c0 = n > 0 ? row.cta_of(unit0) : 0, c1 = n > 0 ? row.cta_of(unit0 + n - 1) : 0;
+    pdl_wait();
+    pdl_trigger();
     if (n == 0) {
         if (lot == 0) g.O[out * D + e] = 0.f;
         if (tid == 0) g.lse[out] = -INFINITY;
         return;
     }
-    const int64_t unit0 = before + n * h;
-    const int c0 = row.cta_of(unit0), c1 = row.cta_of(unit0 + n - 1);
     if (c0 == c1) return;                            // one CTA had all of it
-    // CTA c0 holds the unit's first tiles (its second part, or its first when
-    // it begins there), the others begin inside the unit.
+    // CTA c0 holds the unit's first tiles, in its second part; the others begin
+    // inside the unit, in their first.
     auto part_of = [&](int c) { return g.parts + (2 * (int64_t)c + (c == c0)) * part_floats(g.s); };
-    float M = -INFINITY, l = 0.f, o = 0.f;
-    for (int c = c0 + lot; c <= c1; c += kShare) M = fmaxf(M, part_of(c)[G * D + hd]);
-#pragma unroll 4
-    for (int c = c0 + lot; c <= c1; c += kShare) {
-        const float* p = part_of(c);
-        const float f = ex2(p[G * D + hd] - M);
-        l = fmaf(p[G * D + G + hd], f, l);
-        o = fmaf(p[hd * D + e], f, o);
+    float M = kFloor, l = 0.f, o = 0.f;
+    for (int p0 = c0; p0 <= c1; p0 += kParts) {      // (a second turn only with more than kParts CTAs on a unit)
+        const int m = min(kParts, c1 - p0 + 1);
+        const float* mine = part_of(p0 + (tid < m ? tid : 0)) + G * D + hd;
+        const float r = tid < m ? mine[0] : kFloor, s = tid < m ? mine[G] : 0.f;
+        float top = r;
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+        if (lane == 0) s_red[tid / 32] = top;
+        __syncthreads();
+        top = M;
+#pragma unroll
+        for (int w = 0; w < kThreadsJoin / 32; ++w) top = fmaxf(top, s_red[w]);
+        const float back = ex2(M - top);
+        M = top;
+        o *= back;
+        l *= back;
+        const float f = ex2(r - M);
+        if (tid < m) s_f[tid] = f;
+        float sum = s * f;
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
+        __syncthreads();
+        if (lane == 0) s_red[tid / 32] = sum;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kThreadsJoin / 32; ++w) l += s_red[w];
+#pragma unroll 8
+        for (int c = lot; c < m; c += kShare) o = fmaf(part_of(p0 + c)[hd * D + e], s_f[c], o);
+        __syncthreads();
     }
     s_o[lot][e] = o;
-    if (e == 0) {
-        s_m[lot] = M;
-        s_l[lot] = l;
-    }
     __syncthreads();
     if (lot > 0) return;
-    M = s_m[0];
+    o = s_o[0][e];
 #pragma unroll
-    for (int i = 1; i < kShare; ++i) M = fmaxf(M, s_m[i]);
-    l = o = 0.f;
-#pragma unroll
-    for (int i = 0; i < kShare; ++i) {
-        const float f = s_m[i] == -INFINITY ? 0.f : ex2(s_m[i] - M);
-        l = fmaf(s_l[i], f, l);
-        o = fmaf(s_o[i][e], f, o);
-    }
+    for (int i = 1; i < kShare; ++i) o += s_o[i][e];
     g.O[out * D + e] = o / l;
     if (e == 0) g.lse[out] = (M + log2f(l)) * kLn2;
 }

@@ -41,11 +41,13 @@ __device__ __forceinline__ Unit unit_of(int u, int rot, bool interleaved)
 }
 
 // Raw bits of 8 elements (16 bytes of bf16, two times 16 of float32).
+// load_plain: for rows that the same kernel also writes.
 template <typename T> struct Raw8;
 template <> struct Raw8<__nv_bfloat16> {
     uint4 v;
     __device__ __forceinline__ void load(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
-    __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void load_plain(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = v; }
     __device__ __forceinline__ void widen(float* o) const
     {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -63,7 +65,16 @@ template <> struct Raw8<float> {
         v = __ldg(reinterpret_cast<const uint4*>(p));
         w = __ldg(reinterpret_cast<const uint4*>(p) + 1);
     }
-    __device__ __forceinline__ void zero() { v = w = make_uint4(0u, 0u, 0u, 0u); }
+    __device__ __forceinline__ void load_plain(const float* p)
+    {
+        v = reinterpret_cast<const uint4*>(p)[0];
+        w = reinterpret_cast<const uint4*>(p)[1];
+    }
+    __device__ __forceinline__ void store(float* p) const
+    {
+        reinterpret_cast<uint4*>(p)[0] = v;
+        reinterpret_cast<uint4*>(p)[1] = w;
+    }
     __device__ __forceinline__ void widen(float* o) const
     {
         const uint32_t r[8] = {v.x, v.y, v.z, v.w, w.x, w.y, w.z, w.w};
