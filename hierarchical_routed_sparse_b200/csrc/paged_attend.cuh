@@ -544,35 +544,51 @@ __device__ __forceinline__ void split3(float x0, float x1, uint32_t (&p)[3])
     }
 }
 
-// log2_above of the largest value of rows row0 .. row0 + 15 (two lanes a row).
-template <typename TIn, int D> __device__ __forceinline__ float open_log2(const TIn* v, int row0, int rows, int lane)
-{
-    const int row = row0 + lane / 2;
-    float top = 0.f;
-    if (row < rows) {
-        const uint4* p = reinterpret_cast<const uint4*>(v + row * D + (lane & 1) * (D / 2));
-        constexpr int N = D / 2 * (int)sizeof(TIn) / 16;
+// A lane's values of 16 open rows: rows 2t, 2t + 1 and 8 + 2t, 8 + 2t + 1,
+// d = (D/8) g .. + D/8 - 1; rows that are not there count as zero.
+template <typename TIn, int D> struct OpenValues {
+    static constexpr int N = D / 8 * (int)sizeof(TIn) / 16;      // 16-byte pieces of a row
+    uint4 w[4][N];
+    __device__ __forceinline__ void load(const TIn* v, int row0, int rows, int lane)
+    {
+        const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int row = row0 + 8 * (x / 2) + 2 * t + x % 2;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                w[x][i] = row < rows ? __ldg(reinterpret_cast<const uint4*>(v + row * D + (D / 8) * g) + i)
+                                     : make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+    __device__ __forceinline__ uint32_t word(int x, int i) const
+    {
+        const uint4 q = w[x][i / 4];
+        return i % 4 == 0 ? q.x : i % 4 == 1 ? q.y : i % 4 == 2 ? q.z : q.w;
+    }
+    // log2_above of the tile's largest value.
+    __device__ __forceinline__ float log2_most() const
+    {
+        float top = 0.f;
         if constexpr (sizeof(TIn) == 2) {
             __nv_bfloat162 m = __float2bfloat162_rn(0.f);
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const uint4 w = __ldg(p + i);
-                const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+            for (int x = 0; x < 4; ++x)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(x + e)));
-            }
+                for (int i = 0; i < 4 * N; ++i) {
+                    const uint32_t u = word(x, i);
+                    m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&u)));
+                }
             top = fmaxf(__low2float(m), __high2float(m));
         } else {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const uint4 w = __ldg(p + i);
-                top = fmaxf(fmaxf(fmaxf(top, fabsf(__uint_as_float(w.x))), fabsf(__uint_as_float(w.y))),
-                            fmaxf(fabsf(__uint_as_float(w.z)), fabsf(__uint_as_float(w.w))));
-            }
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int i = 0; i < 4 * N; ++i) top = fmaxf(top, fabsf(__uint_as_float(word(x, i))));
         }
+        return log2_above(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top))));
     }
-    return log2_above(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top))));
-}
+};
 
 // Keys row0 .. row0 + 15 of the open rows (those below `rows`).
 template <typename TIn, int D>
@@ -585,13 +601,21 @@ __device__ __forceinline__ void attend_open(Running<D>& run, const TIn* q, int G
     const bool ha = ra < rows, hz = rz < rows;
     const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
     float s[4] = {0.f, 0.f, 0.f, 0.f}, r[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+    // All of the tile's loads at once, where the registers reach (a tile is one
+    // round trip and a chain of a few hundred instructions).
+    OpenValues<TIn, D> val;
+    if constexpr (!kF32) val.load(v, row0, rows, lane);
+    float4 ka[D / 16], kz[D / 16];
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+        ka[i] = ha ? __ldg(reinterpret_cast<const float4*>(k + ra * D + 16 * i + 4 * t)) : none;
+        kz[i] = hz ? __ldg(reinterpret_cast<const float4*>(k + rz * D + 16 * i + 4 * t)) : none;
+    }
+#pragma unroll
     for (int i = 0; i < D / 16; ++i) {               // d = 16 i + 4 t .. + 3: two products of 8
-        const int d = 16 * i + 4 * t;
-        const float4 xa = ha ? __ldg(reinterpret_cast<const float4*>(k + ra * D + d)) : none;
-        const float4 xz = hz ? __ldg(reinterpret_cast<const float4*>(k + rz * D + d)) : none;
+        const float4 xa = ka[i], xz = kz[i];
         float y[4] = {0.f, 0.f, 0.f, 0.f};
-        if (g < G) load4(q + g * D + d, y);
+        if (g < G) load4(q + g * D + 16 * i + 4 * t, y);
         uint32_t h[8], l[8];
         split_tf32(xa.x, h[0], l[0]);
         split_tf32(xz.x, h[1], l[1]);
@@ -618,7 +642,8 @@ __device__ __forceinline__ void attend_open(Running<D>& run, const TIn* q, int G
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[e] = (e < 2 ? ha : hz) ? (s[e] + r[e]) * scale : -INFINITY;
-    const float lv = open_log2<TIn, D>(v, row0, rows, lane);
+    if constexpr (kF32) val.load(v, row0, rows, lane);
+    const float lv = val.log2_most();
     run.follow(fmaxf(s[0], s[2]) + lv, fmaxf(s[1], s[3]) + lv);
     const float e0 = ex2(s[0] - run.R0), e1 = ex2(s[1] - run.R1), e2 = ex2(s[2] - run.R0), e3 = ex2(s[3] - run.R1);
     run.l0 += e0 + e2;
@@ -631,40 +656,25 @@ __device__ __forceinline__ void attend_open(Running<D>& run, const TIn* q, int G
         w0[i] = transpose8(w0[i]);
         w1[i] = transpose8(w1[i]);
     }
-    // Rows 2t, 2t + 1 and 8 + 2t, 8 + 2t + 1; a row that is not there counts as zero.
-    const int r0 = row0 + 2 * t;
-    const int row[4] = {r0, r0 + 1, r0 + 8, r0 + 9};
 #pragma unroll
-    for (int i = 0; i < D / 16; i += 2) {            // d = (D/8) g + 2i .. + 3
-        const int d = (D / 8) * g + 2 * i;
+    for (int i = 0; i < D / 16; ++i) {               // d = (D/8) g + 2i, + 1
         if constexpr (!kF32) {
-            uint2 w[4];
+            const uint32_t w[4] = {val.word(0, i), val.word(1, i), val.word(2, i), val.word(3, i)};
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-                w[x] = row[x] < rows ? __ldg(reinterpret_cast<const uint2*>(v + row[x] * D + d)) : make_uint2(0u, 0u);
-#pragma unroll
-            for (int x = 2; x >= 0; --x) {
-                mma_bf16(run.acc[i], __byte_perm(w[0].x, w[1].x, 0x5410), __byte_perm(w[0].x, w[1].x, 0x7632),
-                         __byte_perm(w[2].x, w[3].x, 0x5410), __byte_perm(w[2].x, w[3].x, 0x7632), w0[x], w1[x]);
-                mma_bf16(run.acc[i + 1], __byte_perm(w[0].y, w[1].y, 0x5410), __byte_perm(w[0].y, w[1].y, 0x7632),
-                         __byte_perm(w[2].y, w[3].y, 0x5410), __byte_perm(w[2].y, w[3].y, 0x7632), w0[x], w1[x]);
-            }
+            for (int x = 2; x >= 0; --x)
+                mma_bf16(run.acc[i], __byte_perm(w[0], w[1], 0x5410), __byte_perm(w[0], w[1], 0x7632),
+                         __byte_perm(w[2], w[3], 0x5410), __byte_perm(w[2], w[3], 0x7632), w0[x], w1[x]);
         } else {
-            float4 w[4];
+            uint32_t a[4][3];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) w[x] = row[x] < rows ? __ldg(reinterpret_cast<const float4*>(v + row[x] * D + d)) : none;
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                uint32_t a0[3], a1[3], a2[3], a3[3];
-                split3(m ? w[0].z : w[0].x, m ? w[1].z : w[1].x, a0);
-                split3(m ? w[0].w : w[0].y, m ? w[1].w : w[1].y, a1);
-                split3(m ? w[2].z : w[2].x, m ? w[3].z : w[3].x, a2);
-                split3(m ? w[2].w : w[2].y, m ? w[3].w : w[3].y, a3);
-#pragma unroll
-                for (int n = 2; n >= 0; --n)         // parts x of V and n - x of the weights, the smallest first
-#pragma unroll
-                    for (int x = 0; x <= n; ++x) mma_bf16(run.acc[i + m], a0[x], a1[x], a2[x], a3[x], w0[n - x], w1[n - x]);
+            for (int e = 0; e < 2; ++e) {            // d even, odd
+                split3(__uint_as_float(val.word(0, 2 * i + e)), __uint_as_float(val.word(1, 2 * i + e)), a[e]);
+                split3(__uint_as_float(val.word(2, 2 * i + e)), __uint_as_float(val.word(3, 2 * i + e)), a[2 + e]);
             }
+#pragma unroll
+            for (int n = 2; n >= 0; --n)             // parts x of V and n - x of the weights, the smallest first
+#pragma unroll
+                for (int x = 0; x <= n; ++x) mma_bf16(run.acc[i], a[0][x], a[1][x], a[2][x], a[3][x], w0[n - x], w1[n - x]);
         }
     }
 }

@@ -58,9 +58,11 @@ def paged_workspace_size(p: PagedParams) -> int:
 
 def _dense(t, name, shape, dtype, dev):
     """Data pointer of a contiguous tensor on device `dev`, the current one."""
-    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)}")
-    return B._here(t, name, dev)
+    if t.get_device() != dev:
+        B._here(t, name, dev)                        # raises
+    return t.data_ptr()
 
 
 class PagedCache:
@@ -100,11 +102,15 @@ class PagedCache:
         self.workspace = torch.empty(n, dtype=torch.uint8, device=self.table.device) if n else None
         lib = B.load()
         self._append, self._decode = lib.hga_paged_append, lib.hga_paged_decode
+        self._dtype = p.torch_dtype
 
     def _rows(self, t, name, N, H, dev):
-        if t.shape != (N, H, self.p.d) or t.dtype != self.v_tail.dtype or t.stride(2) != 1:
-            raise ValueError(f"{name} must be {self.p.torch_dtype} rows [{N}][{H}][{self.p.d}] with unit stride along d")
-        return B._here(t, name, dev), t.stride(0), t.stride(1)
+        st, sh, sd = t.stride()
+        if t.shape != (N, H, self.p.d) or t.dtype is not self._dtype or sd != 1:
+            raise ValueError(f"{name} must be {self._dtype} rows [{N}][{H}][{self.p.d}] with unit stride along d")
+        if t.get_device() != dev:
+            B._here(t, name, dev)                    # raises
+        return t.data_ptr(), st, sh
 
     def append(self, pos, k, v, cu=None, q=None, q_out=None, rope=None, interleaved: bool = False, stream=None):
         """Tokens cu[b] .. cu[b + 1] - 1 of k, v [N][Hkv][d] (and q [N][Hq][d])
@@ -116,12 +122,11 @@ class PagedCache:
         kp, kt, kh = self._rows(k, "k", N, p.Hkv, dev)
         vp, vt, vh = self._rows(v, "v", N, p.Hkv, dev)
         qp, qt, qh = (None, 0, 0) if q is None else self._rows(q, "q", N, p.Hq, dev)
-        out = None if q_out is None else _dense(q_out, "q_out", (N, p.Hq, p.d), self.v_tail.dtype, dev)
+        out = None if q_out is None else _dense(q_out, "q_out", (N, p.Hq, p.d), self._dtype, dev)
         table, rows, rot = None, 0, 0
         if rope is not None:
-            B._check_table(rope, "rope")
-            table = B._here(rope, "rope", dev)
             rows, rot = rope.shape
+            table = _dense(rope, "rope", (rows, rot), torch.float32, dev)
         code = self._append(
             self._pp, self._pc, _dense(pos, "pos", (p.B,), torch.int32, dev),
             None if cu is None else _dense(cu, "cu", (p.B + 1,), torch.int32, dev), N, qp, qt, qh, kp, kt, kh, vp, vt, vh,
@@ -140,7 +145,7 @@ class PagedCache:
         ws = self.workspace if workspace is None else workspace
         code = self._decode(
             self._pp, self._pc, _dense(pos, "pos", (p.B,), torch.int32, dev),
-            _dense(q, "q", (p.B, p.Hq, p.d), self.v_tail.dtype, dev),
+            _dense(q, "q", (p.B, p.Hq, p.d), self._dtype, dev),
             _dense(O, "O", (p.B, p.Hq, p.d), torch.float32, dev), _dense(lse, "lse", (p.B, p.Hq), torch.float32, dev),
             None if cidx is None else _dense(cidx, "cidx", (p.B, p.Hkv, wc), torch.int32, dev),
             None if gidx is None else _dense(gidx, "gidx", (p.B, p.Hkv, wg), torch.int32, dev),

@@ -12,7 +12,8 @@ in one persistent launch (hga_route_attn_fwd); its backward runs the routed back
 frozen and returns gradients for the segment's Q, K and V (history gets
 none).  ``HGASegmentLayer`` wraps it between real Q / K / V / O projections
 and keeps the KV cache and the summaries of the segments seen so far in
-buffers that grow by doubling (the library reads them in place);
+buffers that grow by doubling (the library reads them in place), and
+``RotaryHeads`` rotates its queries and keys where it has a table;
 ``run_tbptt`` trains a sequence segment by segment (truncated
 back-propagation through time).
 """
@@ -138,16 +139,44 @@ class HGAAttention(torch.autograd.Function):
                 None, None, None, None)
 
 
+class RotaryHeads(torch.autograd.Function):
+    """x [B][T][H][d] rotated by its positions pos0 + t, in the attention's
+    layout [B][H][T][d] and type (hga_rope_fwd); the gradient goes back
+    through the transposed rotation (hga_rope_bwd)."""
+
+    @staticmethod
+    def forward(ctx, x, table, pos0: int, interleaved: bool, dtype):
+        Bn, T, H, d = x.shape
+        if x.stride(3) != 1:
+            x = x.contiguous()
+        y = torch.empty(Bn, H, T, d, device=x.device, dtype=dtype)
+        B.rope_fwd(x, y, table, pos0=pos0, interleaved=interleaved)
+        ctx.save_for_backward(table)
+        ctx.pos0, ctx.interleaved, ctx.shape, ctx.dtype = pos0, interleaved, (Bn, T, H, d), x.dtype
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        table, = ctx.saved_tensors
+        dx = torch.empty(ctx.shape, device=dy.device, dtype=ctx.dtype)
+        B.rope_bwd(dy.contiguous(), dx, table, pos0=ctx.pos0, interleaved=ctx.interleaved)
+        return dx, None, None, None, None
+
+
 class HGASegmentLayer(nn.Module):
     """Attention layer with HGA routed attention: x -> Wq, Wk, Wv (GQA) ->
     HGA -> Wo.  Call ``segment`` once per segment; the layer's KV cache grows
-    by the segment's (detached) keys and values after each call."""
+    by the segment's (detached) keys and values after each call.  With a
+    ``rope`` table (binding.rope_table) queries and keys are rotated by their
+    positions, counted from the start of the cache."""
 
     def __init__(self, d_model: int, Hq: int, Hkv: int, d: int, k_c: int = 8, k_g: int = 32,
-                 dtype=torch.bfloat16, device="cuda"):
+                 dtype=torch.bfloat16, device="cuda", rope=None, interleaved: bool = False):
         super().__init__()
         self.Hq, self.Hkv, self.d, self.k_c, self.k_g = Hq, Hkv, d, k_c, k_g
         self.act_dtype = dtype
+        self.register_buffer("rope", rope, persistent=False)
+        self.interleaved = interleaved
         kw = dict(bias=False, device=device, dtype=torch.float32)
         self.wq = nn.Linear(d_model, Hq * d, **kw)
         self.wk = nn.Linear(d_model, Hkv * d, **kw)
@@ -162,9 +191,13 @@ class HGASegmentLayer(nn.Module):
     def project(self, x):
         """Q [B][Hq][Ts][d], K, V [B][Hkv][Ts][d] of a segment x [B][Ts][d_model]."""
         Bn, Ts, _ = x.shape
-        q = self.wq(x).view(Bn, Ts, self.Hq, self.d).transpose(1, 2)
-        k = self.wk(x).view(Bn, Ts, self.Hkv, self.d).transpose(1, 2)
+        q = self.wq(x).view(Bn, Ts, self.Hq, self.d)
+        k = self.wk(x).view(Bn, Ts, self.Hkv, self.d)
         v = self.wv(x).view(Bn, Ts, self.Hkv, self.d).transpose(1, 2)
+        if self.rope is not None:
+            turn = lambda t: RotaryHeads.apply(t, self.rope, self.cache.T_hist, self.interleaved, self.act_dtype)  # noqa: E731
+            return turn(q), turn(k), v.to(self.act_dtype).contiguous()
+        q, k = q.transpose(1, 2), k.transpose(1, 2)
         return (q.to(self.act_dtype).contiguous(), k.to(self.act_dtype).contiguous(),
                 v.to(self.act_dtype).contiguous())
 
