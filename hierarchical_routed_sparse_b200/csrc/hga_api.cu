@@ -563,6 +563,11 @@ static int run_rope(const hga_rope_params* p, bool back, const void* src, const 
     if (int r = check_stride(p->x_batch, el, "x_batch")) return r;
     if (int r = check_stride(p->x_token, el, "x_token")) return r;
     if (int r = check_stride(p->x_head, el, "x_head")) return r;
+    // Rows that are written must not share elements (what overlaps beyond these
+    // bounds is the caller's to avoid).
+    if (back && ((p->B > 1 && p->x_batch < p->d) || (p->T > 1 && p->x_token < p->d) || (p->H > 1 && p->x_head < p->d)))
+        return fail(HGA_ERR_INVALID_ARG, "rows of dx overlap: strides (%lld, %lld, %lld) below d=%d", (long long)p->x_batch,
+                    (long long)p->x_token, (long long)p->x_head, p->d);
     if (p->T == 0) return HGA_OK;
     if (!src || !dst) return fail(HGA_ERR_INVALID_ARG, "%s: an input or output is NULL", name);
     if (!aligned16(src) || !aligned16(dst))

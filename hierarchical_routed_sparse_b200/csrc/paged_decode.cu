@@ -11,15 +11,15 @@
 // kept groups' held values and the open rows 0 .. p % 64:
 //     O = softmax(scale q K^T) V,  lse = log sum exp (scale q K^T).
 //
-// A cluster of S CTAs (4 warps each) takes one (batch, kv-head).
+// A cluster of S CTAs (of 4 warps, or 6 when S > 1) takes one (batch, kv-head).
 //   * Scoring: CTA r scores the r-th part of the candidates and writes their
 //     keys into every peer's shared memory; each CTA then makes the same
 //     selection (paged_select.cuh).
 //   * Attention: a warp takes tiles of four groups (32 keys), tile i going to
-//     warp i mod 4 S of the cluster, through its own ring of asynchronous
+//     warp i modulo the cluster's warps, through its own ring of asynchronous
 //     copies into mma.sync fragments (paged_attend.cuh).
 //   * Merge: every warp has a running reference, sum and unnormalised output
-//     for each head; the CTA's four meet in shared memory, and each CTA
+//     for each head; a CTA's meet in shared memory, and each CTA
 //     combines d / S elements of every head's output (distributed shared
 //     memory).
 #include "paged.cuh"
@@ -35,7 +35,6 @@ using sm100::cluster_rank;
 using sm100::peer_addr;
 using sm100::smem_u32;
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kMaxS = 8;                             // CTAs per (batch, kv-head)
 constexpr int kSitePage = 421, kSiteLength = 422;
 
@@ -62,7 +61,7 @@ struct Layout {
 };
 __host__ __device__ inline size_t up16(size_t x) { return (x + 15) & ~size_t(15); }
 __host__ __device__ inline size_t larger(size_t a, size_t b) { return a > b ? a : b; }
-template <int D> __host__ __device__ inline Layout layout(const PagedShape& s, int S)
+template <int D, int kWarps> __host__ __device__ inline Layout layout(const PagedShape& s, int S)
 {
     Layout L;
     const size_t nc = s.max_chunks, wc = s.wc, wg = s.wg;
@@ -138,7 +137,7 @@ template <int D> struct Candidates {
         }
     }
 };
-template <int D, typename Row>
+template <int D, int kWarps, typename Row>
 __device__ __forceinline__ void score(const double* us, int c0, int c1, Row row, Key* keys, int warp, int lane)
 {
     constexpr int kAll = Candidates<D>::kStep * kWarps;
@@ -155,6 +154,7 @@ __device__ __forceinline__ void score(const double* us, int c0, int c1, Row row,
 }
 
 // keys[c0, c1) of this CTA into the same slots of its peers.
+template <int kThreads>
 __device__ __forceinline__ void push(Key* keys, int c0, int c1, int S, int rank, int tid)
 {
     const int n = c1 - c0;
@@ -164,16 +164,17 @@ __device__ __forceinline__ void push(Key* keys, int c0, int c1, int S, int rank,
     }
 }
 
-template <typename TIn, int D, int CACHE>
-__global__ void __launch_bounds__(kThreads, 4) paged_decode_kernel(const __grid_constant__ Args g)
+template <typename TIn, int D, int CACHE, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, kWarps == 4 ? 4 : 2) paged_decode_kernel(const __grid_constant__ Args g)
 {
+    constexpr int kThreads = 32 * kWarps;
     extern __shared__ __align__(16) uint8_t sm[];
     __shared__ __align__(16) double us[D];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int S = g.S, rank = S > 1 ? (int)cluster_rank() : 0;
     const int64_t bh = blockIdx.x / S;
     const int b = int(bh / g.s.Hkv), h = int(bh % g.s.Hkv), G = g.s.G;
-    const Layout L = layout<D>(g.s, S);
+    const Layout L = layout<D, kWarps>(g.s, S);
     if (S > 1) cluster_arrive();                     // waited for before the first write to a peer
     pdl_wait();
     pdl_trigger();
@@ -224,14 +225,14 @@ __global__ void __launch_bounds__(kThreads, 4) paged_decode_kernel(const __grid_
     const int kc = g.s.k_c > 0 ? min(g.s.k_c, c0) : c0;
     if (kc < c0) {
         const int b0 = int((int64_t)rank * c0 / S), b1 = int((int64_t)(rank + 1) * c0 / S);
-        score<D>(us, b0, b1, [&](int c) -> const float* {
+        score<D, kWarps>(us, b0, b1, [&](int c) -> const float* {
             const int32_t page = page_of(c);
             return page < 0 ? nullptr : g.c.csum + ((int64_t)page * g.s.Hkv + h) * D;
         }, ckeys, warp, lane);
         __syncthreads();
         if (S > 1) {
             cluster_wait();
-            push(ckeys, b0, b1, S, rank, tid);
+            push<kThreads>(ckeys, b0, b1, S, rank, tid);
             cluster_arrive();
             cluster_wait();
             cluster_arrive();                    // for the groups' push
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 4) paged_decode_kernel(const __grid_
     const int kg = g.s.k_g > 0 ? min(g.s.k_g, n) : n;
     if (kg < n) {
         const int b0 = int((int64_t)rank * n / S), b1 = int((int64_t)(rank + 1) * n / S);
-        score<D>(us, b0, b1, [&](int i) -> const float* {
+        score<D, kWarps>(us, b0, b1, [&](int i) -> const float* {
             const int32_t page = cpage[i / kGroupsPerChunk];
             return page < 0 ? nullptr
                             : g.c.gsum + (((int64_t)page * g.s.Hkv + h) * kGroupsPerChunk + i % kGroupsPerChunk) * D;
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 4) paged_decode_kernel(const __grid_
         __syncthreads();
         if (S > 1) {
             cluster_wait();
-            push(gkeys, b0, b1, S, rank, tid);
+            push<kThreads>(gkeys, b0, b1, S, rank, tid);
             cluster_arrive();
             cluster_wait();
             cluster_arrive();                    // for the merge
@@ -369,15 +370,29 @@ __global__ void __launch_bounds__(kThreads, 4) paged_decode_kernel(const __grid_
     }
 }
 
-template <typename TIn, int D, int CACHE>
-cudaError_t launch(const Args& g, cudaStream_t st)
+// CTAs per (batch, kv-head), a power of two.  Measured at 16K context, k_c 8,
+// k_g 32 (us a call with 1, 2, 4, 8 CTAs): 8 units 21.4, 16.2, 15.3, 14.5; 32
+// units 21.7, 16.3, 15.0, 16.1; 64 units 21.8, 16.4, 17.1, 32.2; 128 units
+// 25.9, 21.0, 36.7; 256 units 35.3, 42.3; 512 units 42.3, 82.1.  At 128K (k_c
+// 16, k_g 64) 32 units take 98, 44, 31, 29.  So: as many as leave a CTA an SM
+// to itself, two CTAs an SM for the first doubling and where there are many
+// chunks to score, and no more than there are chunks to share.
+int split(const PagedShape& s)
 {
-    const size_t smem = layout<D>(g.s, g.S).total;
-    auto k = paged_decode_kernel<TIn, D, CACHE>;
+    const int64_t units = (int64_t)s.B * s.Hkv, sms = sm_count();
+    int S = 1;
+    while (S < kMaxS && S * 4 <= s.max_chunks && units * S * 2 <= (S == 1 || s.max_chunks >= 1024 ? 2 : 1) * sms) S *= 2;
+    return S;
+}
+
+template <typename TIn, int D, int CACHE, int kWarps> cudaError_t launch(const Args& g, cudaStream_t st)
+{
+    const size_t smem = layout<D, kWarps>(g.s, g.S).total;
+    auto k = paged_decode_kernel<TIn, D, CACHE, kWarps>;
     if (cudaError_t e = allow_smem(k, (int)smem)) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(g.s.B * g.s.Hkv * g.S));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(32 * kWarps);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -392,30 +407,16 @@ cudaError_t launch(const Args& g, cudaStream_t st)
     return cudaLaunchKernelEx(&cfg, k, g);
 }
 
-template <typename TIn, int D>
-cudaError_t by_cache(const Args& g, cudaStream_t st)
+template <typename TIn, int D> cudaError_t by_cache(const Args& g, cudaStream_t st)
 {
-    return g.s.cache_dtype == HGA_INT8 ? launch<TIn, D, HGA_INT8>(g, st) : launch<TIn, D, HGA_E4M3>(g, st);
-}
-
-// CTAs per (batch, kv-head), a power of two.  Measured at 16K context, k_c 8,
-// k_g 32 (us a call with 1, 2, 4, 8, 16 CTAs): 8 units 22.3, 18.2, 15.9, 15.3,
-// 16.5; 64 units 22.9, 18.7, 18.0, 20.7, 39.3; 128 units 26.2, 23.2, 23.7,
-// 42.9; 256 units 35.9, 30.5, 48.8; 512 units 42.9, 57.8.  So: two where the
-// GPU holds them all at once, more where it holds them at two a SM, or at
-// four when there are many chunks to score (64K context, 128 units: 82, 57,
-// 44, 77), and no more than chunks to share.
-int split(const PagedShape& s)
-{
-    const int64_t units = (int64_t)s.B * s.Hkv, sms = sm_count();
-    int S = 1;
-    while (S < kMaxS && S * 4 <= s.max_chunks && units * S * 2 <= (S == 1 || s.max_chunks >= 1024 ? 4 : 2) * sms) S *= 2;
-    return S;
+    if (g.s.cache_dtype == HGA_INT8)
+        return g.S > 1 ? launch<TIn, D, HGA_INT8, 6>(g, st) : launch<TIn, D, HGA_INT8, 4>(g, st);
+    return g.S > 1 ? launch<TIn, D, HGA_E4M3, 6>(g, st) : launch<TIn, D, HGA_E4M3, 4>(g, st);
 }
 
 }  // namespace
 
-size_t paged_routed_smem(const PagedShape& s) { return layout<128>(s, kMaxS).total + 2048; }
+size_t paged_routed_smem(const PagedShape& s) { return layout<128, 6>(s, kMaxS).total + 2048; }
 
 cudaError_t launch_paged_routed(const PagedShape& s, const hga_paged_cache& c, const int32_t* pos, const void* q,
                                 float* O, float* lse, int32_t* cidx, int32_t* gidx, cudaStream_t st)

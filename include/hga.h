@@ -345,8 +345,9 @@ int hga_attn_bwd_causal(const hga_params* p, const void* Q, const void* K,
  *   (x_dtype, strided): the transposed rotation, dx1 = dy1 c + dy2 s,
  *   dx2 = dy2 c - dy1 s.  dx rows are overwritten, not accumulated.
  * rot_dim is a multiple of 16 and at most d; strides are non-negative and
- * span multiples of 16 bytes; pos0 + T must not exceed table_rows; T = 0 is
- * no work.  Input and output must not overlap. */
+ * span multiples of 16 bytes (x rows may repeat, stride 0; dx rows may not);
+ * pos0 + T must not exceed table_rows; T = 0 is no work.  Input and output
+ * must not overlap. */
 typedef struct hga_rope_params {
     int     B, H, d;             /* d in {64, 128}                           */
     int     rot_dim, interleaved;
@@ -369,7 +370,7 @@ int hga_rope_bwd(const hga_rope_params* p, const void* dy, const float* table, v
  * the sequence's open rows.
  *   k_pages, v_pages [n_pages][Hkv][64][d]  codes (cache_dtype)
  *   k_scale, v_scale [n_pages][Hkv][8]      float32, one for each 8-token
- *                    group: a value is code * scale
+ *                    group, not negative: a value is code * scale
  *   csum, gsum       [n_pages][Hkv][d], [n_pages][Hkv][8][d]  float32 chunk
  *                    and group summaries (means of the exact keys)
  *   k_tail           [B][Hkv][64][d]  float32: keys of the open chunk
@@ -413,7 +414,8 @@ typedef struct hga_paged_cache {
  * to no sequence (behind cu_tokens[B]) are left alone, in q_out too.
  *   k, v   rows [N][Hkv][d] (dtype) by element strides (token, head), unit
  *          stride along d; q rows [N][Hq][d] alike, or NULL
- *   q_out  [N][Hq][d] (dtype, dense): the rotated queries
+ *   q_out  [N][Hq][d] (dtype, dense): the rotated queries; no overlap with
+ *          the inputs
  *   rope   [rope_rows][rot_dim] as for hga_rope_fwd; rot_dim = 0: the rows
  *          come rotated, or are not to be
  * Keys are rotated in float32 and not rounded again.  A completed group x (8

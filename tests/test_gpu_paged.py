@@ -601,3 +601,77 @@ def test_generation_from_prompts(dtype, kind, k_c, k_g):
             _check_decode(st.cache, kind, pos, st.q, got, rows=st.gidx is not None)
     plain.check(st.cache, _snapshot(st.cache))
     assert hga.device_check() == 0 and hga.device_status() == 0
+
+
+def test_append_many_sequences():
+    # More sequences than lanes, most of them with a token or none, one with
+    # several chunks (a thread counts the chunks of neighbouring sequences).
+    B = 70
+    p = _params(B, 4, 2, 64, 5 * B, 5, "bf16", "int8")
+    c = _cache(p)
+    plain, before = Plain(p, "int8", c.table), _snapshot(c)
+    rope = hga.rope_table(320, 64)
+    rng = np.random.default_rng(3)
+    for i in range(3):
+        lens = rng.integers(0, 3, B).tolist()
+        lens[int(rng.integers(B))] = [170, 64, 40][i]
+        _append(c, plain, lens, 40 + i, rope, False, pad=2)
+    plain.check(c, before)
+    # All of them at a chunk's last token, one token each, without offsets.
+    for b in range(B):
+        have = len(plain.k[b])
+        if have % 64 != 63:
+            n = 63 - have % 64
+            _append(c, plain, [n if x == b else 0 for x in range(B)], 100 + b, rope, False, with_q=False)
+    q, k, v = _tokens(p, B, 7)
+    have = [len(x) for x in plain.k]
+    c.append(_int32(have), k, v, rope=rope)
+    torch.cuda.synchronize()
+    for b in range(B):
+        plain.append(b, k[b:b + 1], v[b:b + 1], rope, False)
+    plain.check(c, before)
+    assert hga.device_check() == 0
+
+
+@pytest.mark.parametrize("n,k_c,k_g", [(60000, 8, 32), (60000, 33, 300), (60000, 200, 700), (60000, -1, 40),
+                                       (140000, 16, 64), (140000, -1, -1)])
+def test_many_chunks(n, k_c, k_g):
+    # Selections of more keys than a warp holds (thinned, or bisected in shared
+    # memory), tables past the part that is staged.
+    p = _params(2, 4, 1, 64, n // 64 + 40, n // 64 + 20, "bf16", "e4m3", k_c, k_g)
+    c = hga.PagedCache(p)
+    g = torch.Generator("cuda").manual_seed(6)
+    for t in (c.k_pages, c.v_pages):
+        t.copy_((torch.randn(t.shape, device="cuda", generator=g) * 60).clamp(-400, 400).to(torch.float8_e4m3fn))
+    for t in (c.k_scale, c.v_scale):
+        t.uniform_(0.003, 0.01, generator=g)
+    for t in (c.csum, c.gsum, c.k_tail):
+        t.normal_(generator=g)
+    c.v_tail.copy_(torch.randn(c.v_tail.shape, device="cuda", generator=g))
+    order = torch.randperm(p.n_pages, device="cuda", generator=g).int()
+    c.table[0, :n // 64] = order[:n // 64]
+    c.table[1, :30] = order[-30:]
+    q = torch.randn(2, 4, 64, device="cuda", generator=g).bfloat16()
+    pos = [n - 1, 1900]
+    rows = k_c > 0 or k_g > 0
+    _check_decode(c, "e4m3", pos, q, _decode(c, pos, q, rows=rows), rows=rows)
+
+
+@pytest.mark.parametrize("size", [1e33, 1e-30])
+def test_queries_of_extreme_size(size):
+    # Scores so far apart that one key takes all the weight, or so near zero
+    # that all keys weigh the same: 2^-20 allows for a weight's two parts, its
+    # exponential and the sums.
+    p = _params(1, 8, 1, 128, 12, 10, "fp32", "int8")
+    c, q = _filled(p, "int8", [600])
+    q = q * size
+    O, lse, _, _ = _decode(c, [599], q, rows=False)
+    pages = c.table[0, :9].long()
+    u8 = lambda t: t[pages].view(torch.uint8).cpu().numpy().reshape(9, 8, 8, 128)  # noqa: E731
+    k = R.held(u8(c.k_pages), c.k_scale[pages, 0].cpu().numpy(), "int8").reshape(-1, 128)
+    v = R.held(u8(c.v_pages), c.v_scale[pages, 0].cpu().numpy(), "int8").reshape(-1, 128)
+    k = np.concatenate([k, c.k_tail[0, 0, :24].double().cpu().numpy()])
+    v = np.concatenate([v, c.v_tail[0, 0, :24].double().cpu().numpy()])
+    o_ref, l_ref = R.attend(q[0].double().cpu().numpy(), k, v, 1 / math.sqrt(128))
+    assert np.abs(O[0] - o_ref).max() <= 2.0 ** -20 * np.abs(v).max()
+    assert (np.abs(lse[0] - l_ref) <= 2.0 ** -20 * (1 + np.abs(l_ref))).all()

@@ -123,6 +123,14 @@ def test_rope_refusals(lib, kw, code):
         assert lib.hga_last_error().decode()
 
 
+def test_gradient_rows_must_not_share_elements(lib):
+    for kw in (dict(x_head=0), dict(x_token=64), dict(x_batch=0)):
+        p = _rope(**kw)
+        assert lib.hga_rope_bwd(ctypes.byref(p), P16, P16, P16, None) == BAD
+        assert lib.hga_rope_fwd(ctypes.byref(p), None, P16, P16, None) == BAD     # (refused for the pointer: fwd may repeat rows)
+        assert "overlap" not in lib.hga_last_error().decode()
+
+
 def test_rope_pointer_refusals(lib):
     p = _rope()
     for a in ((None, P16, P16), (P16, None, P16), (P16, P16, None), (ctypes.c_void_p(4), P16, P16),
