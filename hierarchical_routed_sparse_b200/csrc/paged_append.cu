@@ -303,7 +303,7 @@ __device__ __forceinline__ void rotate_queries(const Args& g, const Seq& q, int 
     const Unit un = unit_of(u, g.a.rot, g.a.interleaved);
     const int r0 = chunk == q.first() ? int(q.pos % kChunk) : 0;
     const int r1 = chunk == q.last() ? int((q.pos + q.n - 1) % kChunk) + 1 : kChunk;
-#pragma unroll 2
+#pragma unroll (Heads > 1 ? 1 : 2)
     for (int r = r0 + (Heads > 1 ? side : 0); r < r1; r += Heads > 1 ? kSide : 1) {
         const int64_t p = (int64_t)chunk * kChunk + r, i = q.token + (p - q.pos);
         const TIn* src = static_cast<const TIn*>(g.a.q.ptr) + i * g.a.q.token;
