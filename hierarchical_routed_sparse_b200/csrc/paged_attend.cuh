@@ -471,44 +471,59 @@ __device__ __forceinline__ void held_outputs(Running<D>& run, const float (&s)[2
 // lane's group (lane / 8) of tile i, called once for each i in order by the
 // whole warp.  Halves K0 V0 K1 V1 ... go round the ring; a copy that is not
 // wanted is an empty group, so that the count of groups says what has landed.
-template <typename TIn, int D, int CACHE, typename GroupOf>
-__device__ __forceinline__ void attend_tiles(Running<D>& run, Half<D>* ring, int n, GroupOf group_of, const TIn* q, int G,
-                                             float scale, const hga_paged_cache& c, int lane)
-{
-    if (n <= 0) return;
-    const auto* kp = static_cast<const uint8_t*>(c.k_pages);
-    const auto* vp = static_cast<const uint8_t*>(c.v_pages);
-    int64_t at = group_of(0);
-    fetch<D, false>(ring[0], kp, c.k_scale, at, lane);
-    fetch_commit();
-    fetch<D, true>(ring[1], vp, c.v_scale, at, lane);
-    fetch_commit();
-    if (n > 1) {
-        at = group_of(1);
-        fetch<D, false>(ring[2], kp, c.k_scale, at, lane);
+// start() begins the first copies; other work of the warp may come between.
+template <typename TIn, int D, int CACHE, typename GroupOf> struct HeldTiles {
+    Half<D>* ring;
+    const hga_paged_cache& c;
+    GroupOf group_of;
+    int n, lane;
+    int64_t at;                                      // the newest tile's group
+
+    __device__ __forceinline__ HeldTiles(Half<D>* ring_, const hga_paged_cache& c_, GroupOf group_of_, int n_, int lane_)
+        : ring(ring_), c(c_), group_of(group_of_), n(n_), lane(lane_), at(-1)
+    {
     }
-    fetch_commit();
-    const Query<TIn, D> qf(q, G, scale, lane);
-    int slot = 0;                                    // of K_i; V_i is in the next
-    for (int i = 0; i < n; ++i) {
-        const int vslot = slot == 2 ? 0 : slot + 1;
-        float s[2][4];
-        fetch_wait();
-        held_scores<TIn, D, CACHE>(s, qf, ring[slot], lane);
-        __syncwarp();
-        if (i + 1 < n) fetch<D, true>(ring[slot], vp, c.v_scale, at, lane);
+    __device__ __forceinline__ void keys(int slot) { fetch<D, false>(ring[slot], static_cast<const uint8_t*>(c.k_pages), c.k_scale, at, lane); }
+    __device__ __forceinline__ void values(int slot) { fetch<D, true>(ring[slot], static_cast<const uint8_t*>(c.v_pages), c.v_scale, at, lane); }
+    __device__ __forceinline__ void start()
+    {
+        if (n <= 0) return;
+        at = group_of(0);
+        keys(0);
         fetch_commit();
-        fetch_wait();
-        held_outputs<D, CACHE>(run, s, ring[vslot], lane);
-        __syncwarp();
-        if (i + 2 < n) {
-            at = group_of(i + 2);
-            fetch<D, false>(ring[vslot], kp, c.k_scale, at, lane);
+        values(1);
+        fetch_commit();
+        if (n > 1) {
+            at = group_of(1);
+            keys(2);
         }
         fetch_commit();
-        slot = vslot == 2 ? 0 : vslot + 1;
     }
-}
+    __device__ __forceinline__ void attend(Running<D>& run, const TIn* q, int G, float scale)
+    {
+        if (n <= 0) return;
+        const Query<TIn, D> qf(q, G, scale, lane);
+        int slot = 0;                                // of K_i; V_i is in the next
+        for (int i = 0; i < n; ++i) {
+            const int vslot = slot == 2 ? 0 : slot + 1;
+            float s[2][4];
+            fetch_wait();
+            held_scores<TIn, D, CACHE>(s, qf, ring[slot], lane);
+            __syncwarp();
+            if (i + 1 < n) values(slot);
+            fetch_commit();
+            fetch_wait();
+            held_outputs<D, CACHE>(run, s, ring[vslot], lane);
+            __syncwarp();
+            if (i + 2 < n) {
+                at = group_of(i + 2);
+                keys(vslot);
+            }
+            fetch_commit();
+            slot = vslot == 2 ? 0 : vslot + 1;
+        }
+    }
+};
 
 // ---- open rows: float32 keys, values in their own type --------------------------------
 // Scores by tf32 products (m16n8k8): a float32 is the sum of two tf32 parts,

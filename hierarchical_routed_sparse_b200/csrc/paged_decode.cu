@@ -308,8 +308,10 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 4 ? 4 : 2) paged_decode
             const int32_t page = u < ng ? gpage[u] : -1;
             return page < 0 ? -1 : ((int64_t)page * g.s.Hkv + h) * kGroupsPerChunk + grow[u] % kGroupsPerChunk;
         };
-        attend_tiles<TIn, D, CACHE>(run, reinterpret_cast<Half<D>*>(sm + L.rings) + kHalves * warp, mine, group_of, q, G,
-                                    g.s.scale * kLog2e, g.c, lane);
+        HeldTiles<TIn, D, CACHE, decltype(group_of)> held(reinterpret_cast<Half<D>*>(sm + L.rings) + kHalves * warp, g.c,
+                                                          group_of, mine, lane);
+        held.start();
+        held.attend(run, q, G, g.s.scale * kLog2e);
     }
 
     // Merge: the CTA's warps, then the cluster's CTAs.  f: a warp's factor for

@@ -55,10 +55,22 @@ __device__ __forceinline__ int64_t tiles_of(const Args& g, int b)
     return 1 + kPerChunk * (p / kChunk);
 }
 
-// What the whole CTA knows of the row of tiles.
-template <int Threads> struct Row {
+// The row of tiles, as every warp finds it for itself: 32 sequences at a time,
+// one a lane.
+struct Row {
     int64_t total;
     int ctas;                                        // CTAs that get tiles
+    __device__ __forceinline__ explicit Row(const Args& g)
+    {
+        int64_t mine = 0;
+#pragma unroll 4
+        for (int b = threadIdx.x & 31; b < g.s.B; b += 32) mine += tiles_of(g, b);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
+        total = mine * g.s.Hkv;
+        const int64_t most = (total + kLeast - 1) / kLeast;
+        ctas = (int)(most < g.grid ? (most > 0 ? most : 1) : g.grid);
+    }
     __device__ __forceinline__ int64_t begin(int cta) const { return total * cta / ctas; }
     __device__ __forceinline__ int cta_of(int64_t tile) const
     {
@@ -68,33 +80,7 @@ template <int Threads> struct Row {
     }
 };
 
-// Sum of `mine` over the CTA, for every thread (synchronises).
-template <int Threads> __device__ __forceinline__ int64_t block_sum(int64_t mine, int64_t* room)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) room[threadIdx.x >> 5] = mine;
-    __syncthreads();
-    int64_t all = 0;
-#pragma unroll
-    for (int w = 0; w < Threads / 32; ++w) all += room[w];
-    return all;
-}
-
-template <int Threads> __device__ __forceinline__ Row<Threads> row_of(const Args& g, int64_t* room)
-{
-    int64_t mine = 0;
-    for (int b = threadIdx.x; b < g.s.B; b += Threads) mine += tiles_of(g, b);
-    Row<Threads> r;
-    r.total = block_sum<Threads>(mine, room) * g.s.Hkv;
-    const int64_t most = (r.total + kLeast - 1) / kLeast;
-    r.ctas = (int)(most < g.grid ? (most > 0 ? most : 1) : g.grid);
-    return r;
-}
-
-// Sequence that holds the tile, and its first unit's first tile.  Every warp
-// looks for itself.
+// Sequence that holds the tile, and its first unit's first tile.
 __device__ __forceinline__ void find(const Args& g, int64_t tile, int& b, int64_t& first)
 {
     const int lane = threadIdx.x & 31;
@@ -132,11 +118,10 @@ template <typename TIn, int D, int CACHE>
 __global__ void __launch_bounds__(kThreads, kPerSm) paged_dense_kernel(const __grid_constant__ Args g)
 {
     extern __shared__ __align__(16) uint8_t sm[];
-    __shared__ int64_t s_room[kWarps];
     pdl_wait();
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = g.s.G;
-    const Row<kThreads> row = row_of<kThreads>(g, s_room);
+    const Row row(g);
     if ((int)blockIdx.x >= row.ctas || row.total == 0) return;
     int64_t at = row.begin(blockIdx.x);
     const int64_t end = row.begin(blockIdx.x + 1);
@@ -158,15 +143,6 @@ __global__ void __launch_bounds__(kThreads, kPerSm) paged_dense_kernel(const __g
         const TIn* q = static_cast<const TIn*>(g.q) + head0 * D;
         const int32_t* table = g.c.table + (int64_t)b * g.s.max_chunks;
 
-        Running<D> run;
-        run.init();
-        if (from == 0) {                             // the open rows
-            const int rows = int(g.pos[b] % kChunk) + 1;
-            const int64_t r0 = bh * kChunk * D;
-            if (16 * warp < rows)
-                attend_open<TIn, D>(run, q, G, g.c.k_tail + r0, static_cast<const TIn*>(g.c.v_tail) + r0, 16 * warp, rows,
-                                    g.s.scale * kLog2e, lane);
-        }
         // Tile j > 0 is half (j - 1) % 2 of chunk (j - 1) / 2.  A CTA's last warp
         // begins, since the first ones have open rows.
         const int64_t j0 = (from > 0 ? from : 1) - 1 + (kWarps - 1 - warp), j1 = to - 1;
@@ -184,8 +160,19 @@ __global__ void __launch_bounds__(kThreads, kPerSm) paged_dense_kernel(const __g
             const int32_t page = __shfl_sync(0xFFFFFFFFu, pages, i % 32);
             return page < 0 ? -1 : (int64_t)page * page_groups + in_page;
         };
-        attend_tiles<TIn, D, CACHE>(run, reinterpret_cast<Half<D>*>(sm) + kHalves * warp, mine, group_of, q, G,
-                                    g.s.scale * kLog2e, g.c, lane);
+        HeldTiles<TIn, D, CACHE, decltype(group_of)> held(reinterpret_cast<Half<D>*>(sm) + kHalves * warp, g.c, group_of, mine,
+                                                          lane);
+        held.start();
+        Running<D> run;
+        run.init();
+        if (from == 0) {                             // the open rows
+            const int rows = int(g.pos[b] % kChunk) + 1;
+            const int64_t r0 = bh * kChunk * D;
+            if (16 * warp < rows)
+                attend_open<TIn, D>(run, q, G, g.c.k_tail + r0, static_cast<const TIn*>(g.c.v_tail) + r0, 16 * warp, rows,
+                                    g.s.scale * kLog2e, lane);
+        }
+        held.attend(run, q, G, g.s.scale * kLog2e);
 
         // The warps' parts meet; f: a warp's factor.
         __syncthreads();
@@ -234,18 +221,19 @@ constexpr int kShare = 4, kParts = 256;              // parts whose factors are 
 template <int D> __global__ void __launch_bounds__(kShare * D) paged_join_kernel(const __grid_constant__ Args g)
 {
     constexpr int kThreadsJoin = kShare * D;
-    __shared__ int64_t s_room[kThreadsJoin / 32];
     __shared__ float s_o[kShare][D], s_f[kParts], s_red[kThreadsJoin / 32];
     const int tid = threadIdx.x, e = tid % D, lot = tid / D, lane = tid & 31, G = g.s.G;
     const int64_t bh = blockIdx.x / G;
     const int hd = blockIdx.x % G, b = int(bh / g.s.Hkv), h = int(bh % g.s.Hkv);
     const int64_t out = (int64_t)b * g.s.Hq + h * G + hd;
+    const Row row(g);
     int64_t before = 0;
-    for (int i = tid; i < b; i += kThreadsJoin) before += tiles_of(g, i);
-    const Row<kThreadsJoin> row = row_of<kThreadsJoin>(g, s_room);
-    before = block_sum<kThreadsJoin>(before, s_room) * g.s.Hkv;
+#pragma unroll 4
+    for (int i = lane; i < b; i += 32) before += tiles_of(g, i);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, x);
     const int64_t n = tiles_of(g, b);
-    const int64_t unit0 = before + n * h;
+    const int64_t unit0 = before * g.s.Hkv + n * h;
     const int c0 = n > 0 ? row.cta_of(unit0) : 0, c1 = n > 0 ? row.cta_of(unit0 + n - 1) : 0;
     pdl_wait();
     pdl_trigger();
