@@ -725,6 +725,8 @@ int hga_paged_decode(const hga_paged_params* p, const hga_paged_cache* c, const 
                         s.max_chunks, s.wc);
         return finish(hga::launch_paged_routed(s, *c, pos, q, O, lse, cidx, gidx, st), st, "hga_paged_decode");
     }
+    if (!hga::paged_dense_fits(s))
+        return fail(HGA_ERR_UNSUPPORTED, "%d sequences of %d chunks: too many for one dense call", s.B, s.max_chunks);
     CHECK_PTR(workspace);
     const size_t need = hga::paged_dense_workspace(s);
     if (ws_bytes < need)

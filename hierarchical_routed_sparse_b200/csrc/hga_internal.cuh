@@ -237,6 +237,7 @@ size_t paged_routed_smem(const PagedShape& s);
 cudaError_t launch_paged_dense(const PagedShape& s, const hga_paged_cache& c, const int32_t* pos, const void* q,
                                float* O, float* lse, void* workspace, cudaStream_t st);
 size_t paged_dense_workspace(const PagedShape& s);
+bool paged_dense_fits(const PagedShape& s);
 
 // Streaming multiprocessors of the current device (cached per device).
 int sm_count();

@@ -38,15 +38,16 @@ struct Args {
     const void* q;
     float* O;
     float* lse;
-    float* parts;                                    // [grid][2][G d + 2 G]
+    float* parts;                                    // [grid][2][part_floats]
     int grid;                                        // CTAs of the first kernel
 };
 
 // Tiles of a sequence's units: none when it is empty (or its position is
-// past the table: recorded).
-__device__ __forceinline__ int64_t tiles_of(const Args& g, int b)
+// past the table: recorded).  The sum over all units is below 2^31 (checked
+// on the host).
+__device__ __forceinline__ int tiles_of(const Args& g, int b)
 {
-    const int64_t p = g.pos[b];
+    const int32_t p = g.pos[b];
     if (p < 0) return 0;
     if (p >= (int64_t)g.s.max_chunks * kChunk) {
         flag(kSiteLength);
@@ -55,42 +56,44 @@ __device__ __forceinline__ int64_t tiles_of(const Args& g, int b)
     return 1 + kPerChunk * (p / kChunk);
 }
 
+__device__ __forceinline__ int warp_sum_int(int v) { return __reduce_add_sync(0xFFFFFFFFu, v); }
+
 // The row of tiles, as every warp finds it for itself: 32 sequences at a time,
-// one a lane.
+// one a lane.  CTA i's first tile is i * least + min(i, more).
 struct Row {
-    int64_t total;
-    int ctas;                                        // CTAs that get tiles
+    int total, ctas, least, more;                    // ctas: those that get tiles
+    int lane_tiles;                                  // of sequence `lane`, when there are at most 32
     __device__ __forceinline__ explicit Row(const Args& g)
     {
-        int64_t mine = 0;
+        const int lane = threadIdx.x & 31;
+        lane_tiles = 0;
+        int mine = 0;
 #pragma unroll 4
-        for (int b = threadIdx.x & 31; b < g.s.B; b += 32) mine += tiles_of(g, b);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
-        total = mine * g.s.Hkv;
-        const int64_t most = (total + kLeast - 1) / kLeast;
-        ctas = (int)(most < g.grid ? (most > 0 ? most : 1) : g.grid);
+        for (int b = lane; b < g.s.B; b += 32) mine += lane_tiles = tiles_of(g, b);
+        total = warp_sum_int(mine) * g.s.Hkv;
+        ctas = max(1, min(g.grid, (total + kLeast - 1) / kLeast));
+        least = total / ctas;
+        more = total - least * ctas;
     }
-    __device__ __forceinline__ int64_t begin(int cta) const { return total * cta / ctas; }
-    __device__ __forceinline__ int cta_of(int64_t tile) const
+    __device__ __forceinline__ int begin(int cta) const { return cta * least + min(cta, more); }
+    __device__ __forceinline__ int cta_of(int tile) const
     {
-        int i = int(tile * ctas / total);
-        while (begin(i + 1) <= tile) ++i;
-        return i;
+        const int big = more * (least + 1);          // tiles of the CTAs that have one more
+        return tile < big ? tile / (least + 1) : more + (tile - big) / least;
     }
 };
 
 // Sequence that holds the tile, and its first unit's first tile.
-__device__ __forceinline__ void find(const Args& g, int64_t tile, int& b, int64_t& first)
+__device__ __forceinline__ void find(const Args& g, const Row& row, int tile, int& b, int& first)
 {
     const int lane = threadIdx.x & 31;
     first = 0;
     for (int b0 = 0; b0 < g.s.B; b0 += 32) {
-        const int64_t n = b0 + lane < g.s.B ? tiles_of(g, b0 + lane) * g.s.Hkv : 0;
-        int64_t upto = n;
+        const int n = (g.s.B <= 32 ? row.lane_tiles : b0 + lane < g.s.B ? tiles_of(g, b0 + lane) : 0) * g.s.Hkv;
+        int upto = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+            const int v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
             if (lane >= o) upto += v;
         }
         const unsigned hit = __ballot_sync(0xFFFFFFFFu, tile < first + upto);
@@ -105,7 +108,8 @@ __device__ __forceinline__ void find(const Args& g, int64_t tile, int& b, int64_
     b = g.s.B;
 }
 
-__host__ __device__ inline size_t part_floats(const PagedShape& s) { return (size_t)s.G * s.d + 2 * (size_t)s.G; }
+// (A multiple of 4 floats, as a part's rows are read.)
+__host__ __device__ inline size_t part_floats(const PagedShape& s) { return ((size_t)s.G * s.d + 2 * (size_t)s.G + 3) & ~size_t(3); }
 
 template <int D> constexpr size_t rings_bytes() { return sizeof(Half<D>) * kHalves * kWarps; }
 template <int D> inline size_t dense_smem(const PagedShape& s)
@@ -123,34 +127,33 @@ __global__ void __launch_bounds__(kThreads, kPerSm) paged_dense_kernel(const __g
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = g.s.G;
     const Row row(g);
     if ((int)blockIdx.x >= row.ctas || row.total == 0) return;
-    int64_t at = row.begin(blockIdx.x);
-    const int64_t end = row.begin(blockIdx.x + 1);
-    int b;
-    int64_t first;                                   // of the sequence's first unit
-    find(g, at, b, first);
+    int at = row.begin(blockIdx.x);
+    const int end = row.begin(blockIdx.x + 1);
+    int b, first;                                    // first: of the sequence's first unit
+    find(g, row, at, b, first);
 
     while (at < end) {
-        const int64_t n = tiles_of(g, b);
+        const int n = tiles_of(g, b);
         if (n == 0 || at >= first + n * g.s.Hkv) {   // to the next sequence
             first += n * g.s.Hkv;
             ++b;
             continue;
         }
-        const int h = int((at - first) / n);
-        const int64_t unit0 = first + n * h;         // the unit's tiles: unit0 .. unit0 + n - 1
-        const int64_t from = at - unit0, to = end - unit0 < n ? end - unit0 : n;
+        const int h = (at - first) / n;
+        const int unit0 = first + n * h;             // the unit's tiles: unit0 .. unit0 + n - 1
+        const int from = at - unit0, to = end - unit0 < n ? end - unit0 : n;
         const int64_t bh = (int64_t)b * g.s.Hkv + h, head0 = (int64_t)b * g.s.Hq + h * G;
         const TIn* q = static_cast<const TIn*>(g.q) + head0 * D;
         const int32_t* table = g.c.table + (int64_t)b * g.s.max_chunks;
 
         // Tile j > 0 is half (j - 1) % 2 of chunk (j - 1) / 2.  A CTA's last warp
         // begins, since the first ones have open rows.
-        const int64_t j0 = (from > 0 ? from : 1) - 1 + (kWarps - 1 - warp), j1 = to - 1;
-        const int mine = j1 > j0 ? int((j1 - j0 + kWarps - 1) / kWarps) : 0;
+        const int j0 = (from > 0 ? from : 1) - 1 + (kWarps - 1 - warp), j1 = to - 1;
+        const int mine = j1 > j0 ? (j1 - j0 + kWarps - 1) / kWarps : 0;
         int32_t pages = 0;                           // pages of 32 of the warp's tiles, one a lane
         static_assert(kWarps % kPerChunk == 0, "a warp's tiles are the same part of their chunks");
-        const int64_t chunk0 = j0 / kPerChunk;
-        const int in_page = h * kGroupsPerChunk + kTileGroups * int(j0 % kPerChunk) + lane / 8;
+        const int chunk0 = j0 / kPerChunk;
+        const int in_page = h * kGroupsPerChunk + kTileGroups * (j0 % kPerChunk) + lane / 8;
         const int page_groups = g.s.Hkv * kGroupsPerChunk;
         auto group_of = [&](int i) -> int64_t {
             if (i % 32 == 0)
@@ -213,78 +216,87 @@ __global__ void __launch_bounds__(kThreads, kPerSm) paged_dense_kernel(const __g
 }
 
 // One unit and head a CTA: joins the parts of a unit that several CTAs hold,
-// and writes the outputs of empty sequences.  kShare threads share an
-// element's parts.  Until pdl_wait only the caller's inputs are read: the
-// first kernel's CTAs let this one start after their own wait, when whatever
-// wrote the inputs is done.
-constexpr int kShare = 4, kParts = 256;              // parts whose factors are formed at once
-template <int D> __global__ void __launch_bounds__(kShare * D) paged_join_kernel(const __grid_constant__ Args g)
+// and writes the outputs of empty sequences.  A part is read by D/4 threads,
+// four elements each, kLots parts at a time.  Until pdl_wait only the caller's
+// inputs are read: the first kernel's CTAs let this one start after their own
+// wait, when whatever wrote the inputs is done.
+constexpr int kJoinThreads = 512, kParts = 256;      // parts whose factors are formed at once
+template <int D> __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ Args g)
 {
-    constexpr int kThreadsJoin = kShare * D;
-    __shared__ float s_o[kShare][D], s_f[kParts], s_red[kThreadsJoin / 32];
-    const int tid = threadIdx.x, e = tid % D, lot = tid / D, lane = tid & 31, G = g.s.G;
+    constexpr int kLots = kJoinThreads / (D / 4), kJoinWarps = kJoinThreads / 32;
+    __shared__ float4 s_o[kLots][D / 4];
+    __shared__ float s_f[kParts], s_red[2][kJoinWarps];
+    const int tid = threadIdx.x, e = tid % (D / 4), lot = tid / (D / 4), lane = tid & 31, G = g.s.G;
     const int64_t bh = blockIdx.x / G;
     const int hd = blockIdx.x % G, b = int(bh / g.s.Hkv), h = int(bh % g.s.Hkv);
     const int64_t out = (int64_t)b * g.s.Hq + h * G + hd;
     const Row row(g);
-    int64_t before = 0;
+    int before = 0;
 #pragma unroll 4
     for (int i = lane; i < b; i += 32) before += tiles_of(g, i);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) before += __shfl_xor_sync(0xFFFFFFFFu, before, x);
-    const int64_t n = tiles_of(g, b);
-    const int64_t unit0 = before * g.s.Hkv + n * h;
+    const int n = tiles_of(g, b), unit0 = warp_sum_int(before) * g.s.Hkv + n * h;
     const int c0 = n > 0 ? row.cta_of(unit0) : 0, c1 = n > 0 ? row.cta_of(unit0 + n - 1) : 0;
     pdl_wait();
     pdl_trigger();
     if (n == 0) {
-        if (lot == 0) g.O[out * D + e] = 0.f;
+        if (lot == 0) reinterpret_cast<float4*>(g.O + out * D)[e] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (tid == 0) g.lse[out] = -INFINITY;
         return;
     }
     if (c0 == c1) return;                            // one CTA had all of it
     // CTA c0 holds the unit's first tiles, in its second part; the others begin
     // inside the unit, in their first.
-    auto part_of = [&](int c) { return g.parts + (2 * (int64_t)c + (c == c0)) * part_floats(g.s); };
-    float M = kFloor, l = 0.f, o = 0.f;
+    const size_t stride = part_floats(g.s);
+    auto part_of = [&](int c) { return g.parts + (2 * (int64_t)c + (c == c0)) * stride; };
+    float M = kFloor, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int p0 = c0; p0 <= c1; p0 += kParts) {      // (a second turn only with more than kParts CTAs on a unit)
         const int m = min(kParts, c1 - p0 + 1);
-        const float* mine = part_of(p0 + (tid < m ? tid : 0)) + G * D + hd;
-        const float r = tid < m ? mine[0] : kFloor, s = tid < m ? mine[G] : 0.f;
+        float r = kFloor, s = 0.f;
+        if (tid < m) {
+            const float* mine = part_of(p0 + tid) + G * D + hd;
+            r = mine[0];
+            s = mine[G];
+        }
         float top = r;
 #pragma unroll
         for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
-        if (lane == 0) s_red[tid / 32] = top;
+        if (lane == 0) s_red[0][tid / 32] = top;
         __syncthreads();
         top = M;
 #pragma unroll
-        for (int w = 0; w < kThreadsJoin / 32; ++w) top = fmaxf(top, s_red[w]);
-        const float back = ex2(M - top);
+        for (int w = 0; w < kParts / 32; ++w) top = fmaxf(top, s_red[0][w]);
+        const float back = ex2(M - top), f = ex2(r - top);
         M = top;
-        o *= back;
-        l *= back;
-        const float f = ex2(r - M);
         if (tid < m) s_f[tid] = f;
         float sum = s * f;
 #pragma unroll
         for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
+        if (lane == 0) s_red[1][tid / 32] = sum;
         __syncthreads();
-        if (lane == 0) s_red[tid / 32] = sum;
-        __syncthreads();
+        l *= back;
 #pragma unroll
-        for (int w = 0; w < kThreadsJoin / 32; ++w) l += s_red[w];
+        for (int w = 0; w < kParts / 32; ++w) l += s_red[1][w];
+        o.x *= back; o.y *= back; o.z *= back; o.w *= back;
 #pragma unroll 8
-        for (int c = lot; c < m; c += kShare) o = fmaf(part_of(p0 + c)[hd * D + e], s_f[c], o);
-        __syncthreads();
+        for (int c = lot; c < m; c += kLots) {
+            const float4 v = reinterpret_cast<const float4*>(part_of(p0 + c) + hd * D)[e];
+            const float x = s_f[c];
+            o.x = fmaf(v.x, x, o.x);
+            o.y = fmaf(v.y, x, o.y);
+            o.z = fmaf(v.z, x, o.z);
+            o.w = fmaf(v.w, x, o.w);
+        }
+        __syncthreads();                             // s_f may be written again
     }
     s_o[lot][e] = o;
     __syncthreads();
-    if (lot > 0) return;
-    o = s_o[0][e];
+    if (tid >= D) return;
+    float sum = 0.f;
 #pragma unroll
-    for (int i = 1; i < kShare; ++i) o += s_o[i][e];
-    g.O[out * D + e] = o / l;
-    if (e == 0) g.lse[out] = (M + log2f(l)) * kLn2;
+    for (int i = 0; i < kLots; ++i) sum += reinterpret_cast<const float*>(s_o[i])[tid];
+    g.O[out * D + tid] = sum / l;
+    if (tid == 0) g.lse[out] = (M + log2f(l)) * kLn2;
 }
 
 template <typename TIn, int D, int CACHE> cudaError_t launch(const Args& g, cudaStream_t st)
@@ -293,7 +305,7 @@ template <typename TIn, int D, int CACHE> cudaError_t launch(const Args& g, cuda
     const size_t smem = dense_smem<D>(g.s);
     if (cudaError_t e = allow_smem(k, (int)smem)) return e;
     if (cudaError_t e = launch_pdl(k, dim3((unsigned)g.grid), dim3(kThreads), smem, st, g)) return e;
-    return launch_pdl(paged_join_kernel<D>, dim3((unsigned)(g.s.B * g.s.Hq)), dim3(kShare * D), 0, st, g);
+    return launch_pdl(paged_join_kernel<D>, dim3((unsigned)(g.s.B * g.s.Hq)), dim3(kJoinThreads), 0, st, g);
 }
 
 template <typename TIn, int D> cudaError_t by_cache(const Args& g, cudaStream_t st)
@@ -302,6 +314,12 @@ template <typename TIn, int D> cudaError_t by_cache(const Args& g, cudaStream_t 
 }
 
 }  // namespace
+
+// The tiles of all units are counted in 32 bits.
+bool paged_dense_fits(const PagedShape& s)
+{
+    return (int64_t)s.B * s.Hkv * (1 + kPerChunk * (int64_t)s.max_chunks) <= INT32_MAX - kLeast;
+}
 
 size_t paged_dense_workspace(const PagedShape& s) { return sizeof(float) * part_floats(s) * 2 * kPerSm * (size_t)sm_count(); }
 

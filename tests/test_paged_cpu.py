@@ -99,6 +99,7 @@ def test_decode_refusals(lib):
     assert need > 0 and hga.paged_workspace_size(_paged()) == 0
     assert call(dense, cidx=None, gidx=None, n=need - 1) == BAD
     assert call(dense, cidx=None, gidx=None, ws=None) == BAD
+    assert call(_paged(k_c=hga.HGA_ALL, k_g=hga.HGA_ALL, B=1 << 12, max_chunks=1 << 18), cidx=None, gidx=None) == UNSUP
     assert call(dense, cidx=None, gidx=None, ws=ctypes.c_void_p(4)) == BAD
     assert call(_paged(Hq=18, Hkv=2)) == UNSUP                                    # 9 q-heads per kv-head
     assert call(_paged(k_c=1 << 14, max_chunks=1 << 14)) == UNSUP                 # routing state past shared memory
