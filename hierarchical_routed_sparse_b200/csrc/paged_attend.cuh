@@ -232,6 +232,22 @@ __device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&y)[4])
     y[2] = __uint_as_float(w.y << 16); y[3] = __uint_as_float(w.y & 0xFFFF0000u);
 }
 
+// The references and sums of one head's parts, one part a lane of N neighbours
+// (a power of two): r becomes the common reference, l the sum for it; returns
+// the part's factor.  The whole warp takes part.
+template <int N> __device__ __forceinline__ float join_parts(float& r, float& l)
+{
+    float M = r;
+#pragma unroll
+    for (int o = 1; o < N; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+    const float f = ex2(r - M);
+    l *= f;
+#pragma unroll
+    for (int o = 1; o < N; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+    r = M;
+    return f;
+}
+
 // The query as the products' B operand, and what turns a product into a
 // score in log2 units, for heads 2t, 2t + 1.
 template <typename TIn, int D> struct Query {

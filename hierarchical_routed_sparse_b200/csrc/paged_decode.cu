@@ -41,7 +41,7 @@ using sm100::cluster_rank;
 using sm100::peer_addr;
 using sm100::smem_u32;
 
-constexpr int kMaxS = 8;                             // CTAs per (batch, kv-head)
+constexpr int kMaxS = 8;                             // CTAs per (batch, kv-head); warps of one are at most as many
 constexpr int kSitePage = 421, kSiteLength = 422;
 
 struct Args {
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 4 ? 4 : 2) paged_decode
     }
 
     // Attention.
-    const int wid = rank * kWarps + warp, n_workers = S * kWarps;
+    const int wid = warp * S + rank, n_workers = S * kWarps;     // neighbouring tiles on different SMs
     Running<D> run;
     run.init();
     if (warp > 0 && own_tile) run.unpark(parked, lane);
@@ -329,20 +329,19 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 4 ? 4 : 2) paged_decode
     float* ibl = ibr + S * G;
     float* ibf = ibl + S * G;
     if (S > 1) cluster_wait();                       // (of the start, or of the last exchange)
-    for (int i = tid; i < kWarps * G; i += kThreads) {
-        const int hd = i % G;
-        float M = rm[hd];
-        for (int w = 1; w < kWarps; ++w) M = fmaxf(M, rm[w * G + hd]);
-        float l = 0.f;
-        for (int w = 0; w < kWarps; ++w) l = fmaf(lm[w * G + hd], ex2(rm[w * G + hd] - M), l);
-        const float f = ex2(rm[i] - M);
-        fm[i] = S > 1 ? f : f / l;
+    // A head's warps, then its CTAs, are eight neighbouring lanes.
+    if (warp < (8 * G + 31) / 32) {
+        const int hd = tid / 8, w = tid % 8;
+        const bool is = hd < G && w < kWarps;
+        float M = is ? rm[w * G + hd] : kFloor, l = is ? lm[w * G + hd] : 0.f;
+        const float f = join_parts<8>(M, l);
+        if (is) fm[w * G + hd] = S > 1 ? f : f / l;
         if (S > 1) {
-            for (int to = i / G; to < S; to += kWarps) {
-                sm100::st_cluster_f32(peer_addr(smem_u32(ibr + rank * G + hd), to), M);
-                sm100::st_cluster_f32(peer_addr(smem_u32(ibl + rank * G + hd), to), l);
+            if (hd < G && w < S) {
+                sm100::st_cluster_f32(peer_addr(smem_u32(ibr + rank * G + hd), w), M);
+                sm100::st_cluster_f32(peer_addr(smem_u32(ibl + rank * G + hd), w), l);
             }
-        } else if (i < G) {
+        } else if (is && w == 0) {
             g.lse[head0 + hd] = (M + log2f(l)) * kLn2;
         }
     }
@@ -360,14 +359,13 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 4 ? 4 : 2) paged_decode
     if (S == 1) return;
     cluster_arrive();
     cluster_wait();
-    for (int i = tid; i < S * G; i += kThreads) {
-        const int hd = i % G;
-        float M = ibr[hd];
-        for (int c = 1; c < S; ++c) M = fmaxf(M, ibr[c * G + hd]);
-        float l = 0.f;
-        for (int c = 0; c < S; ++c) l = fmaf(ibl[c * G + hd], ex2(ibr[c * G + hd] - M), l);
-        ibf[i] = ex2(ibr[i] - M) / l;
-        if (i < G && rank == 0) g.lse[head0 + hd] = (M + log2f(l)) * kLn2;
+    if (warp < (8 * G + 31) / 32) {
+        const int hd = tid / 8, c = tid % 8;
+        const bool is = hd < G && c < S;
+        float M = is ? ibr[c * G + hd] : kFloor, l = is ? ibl[c * G + hd] : 0.f;
+        const float f = join_parts<8>(M, l);
+        if (is) ibf[c * G + hd] = f / l;
+        if (is && c == 0 && rank == 0) g.lse[head0 + hd] = (M + log2f(l)) * kLn2;
     }
     __syncthreads();
     for (int i = tid; i < G * part; i += kThreads) {

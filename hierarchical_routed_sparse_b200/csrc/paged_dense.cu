@@ -187,13 +187,13 @@ __global__ void __launch_bounds__(kThreads, kPerSm) paged_dense_kernel(const __g
         __syncthreads();
         const bool whole = from == 0 && to == n;
         float* part = g.parts + (2 * (int64_t)blockIdx.x + (from == 0)) * part_floats(g.s);
-        for (int i = tid; i < kWarps * G; i += kThreads) {
-            const int hd = i % G;
-            float M = rm[hd], l = 0.f;
-            for (int w = 1; w < kWarps; ++w) M = fmaxf(M, rm[w * G + hd]);
-            for (int w = 0; w < kWarps; ++w) l = fmaf(lm[w * G + hd], ex2(rm[w * G + hd] - M), l);
-            fm[i] = whole ? ex2(rm[i] - M) / l : ex2(rm[i] - M);
-            if (i < G) {
+        if (warp < (8 * G + 31) / 32) {              // a head's warps are eight neighbouring lanes
+            const int hd = tid / 8, w = tid % 8;
+            const bool is = hd < G && w < kWarps;
+            float M = is ? rm[w * G + hd] : kFloor, l = is ? lm[w * G + hd] : 0.f;
+            const float f = join_parts<8>(M, l);
+            if (is) fm[w * G + hd] = whole ? f / l : f;
+            if (is && w == 0) {
                 if (whole) {
                     g.lse[head0 + hd] = (M + log2f(l)) * kLn2;
                 } else {
