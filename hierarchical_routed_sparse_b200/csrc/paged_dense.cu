@@ -4,9 +4,9 @@
 //
 // The sequences of a batch differ in length, and one long sequence may be all
 // there is, so work is cut by keys and not by sequences: the tiles (32 keys)
-// of all units (batch, kv-head) stand in one row, each unit's led by one that
-// stands for its open rows, and every CTA takes the same number of
-// neighbours.  A unit that one CTA holds from end to end is finished there;
+// of all units (batch, kv-head) stand in one row, each unit's led by kOpen that
+// stand for its open rows (and for what a unit costs whatever its length), and
+// every CTA takes the same number of neighbours.  A unit that one CTA holds from end to end is finished there;
 // the parts of the others (output, reference and sum of each head) go to the
 // workspace, and a second kernel joins them.  Which CTA has what follows from
 // the positions, which both kernels read on the device.
@@ -28,6 +28,7 @@ using namespace paged;
 // registers: 43.4 us where this takes 40.6, 8 sequences of up to 16K).
 constexpr int kWarps = 6, kThreads = 32 * kWarps, kPerSm = 2;
 constexpr int kLeast = 2 * kWarps;                   // tiles of a CTA, where there are few
+constexpr int kOpen = kLeast;                        // tiles that a unit's open rows, start and merge count as
 constexpr int kPerChunk = kGroupsPerChunk / kTileGroups;
 constexpr int kSitePage = 431, kSiteLength = 432;
 
@@ -53,7 +54,7 @@ __device__ __forceinline__ int tiles_of(const Args& g, int b)
         flag(kSiteLength);
         return 0;
     }
-    return 1 + kPerChunk * (p / kChunk);
+    return kOpen + kPerChunk * (p / kChunk);
 }
 
 __device__ __forceinline__ int warp_sum_int(int v) { return __reduce_add_sync(0xFFFFFFFFu, v); }
@@ -146,9 +147,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm) paged_dense_kernel(const __g
         const TIn* q = static_cast<const TIn*>(g.q) + head0 * D;
         const int32_t* table = g.c.table + (int64_t)b * g.s.max_chunks;
 
-        // Tile j > 0 is half (j - 1) % 2 of chunk (j - 1) / 2.  A CTA's last warp
-        // begins, since the first ones have open rows.
-        const int j0 = (from > 0 ? from : 1) - 1 + (kWarps - 1 - warp), j1 = to - 1;
+        // Tile kOpen + j is half j % 2 of chunk j / 2.  A CTA's last warp begins,
+        // since the first ones have open rows.
+        const int j0 = max(from - kOpen, 0) + (kWarps - 1 - warp), j1 = to - kOpen;
         const int mine = j1 > j0 ? (j1 - j0 + kWarps - 1) / kWarps : 0;
         int32_t pages = 0;                           // pages of 32 of the warp's tiles, one a lane
         static_assert(kWarps % kPerChunk == 0, "a warp's tiles are the same part of their chunks");
@@ -318,7 +319,7 @@ template <typename TIn, int D> cudaError_t by_cache(const Args& g, cudaStream_t 
 // The tiles of all units are counted in 32 bits.
 bool paged_dense_fits(const PagedShape& s)
 {
-    return (int64_t)s.B * s.Hkv * (1 + kPerChunk * (int64_t)s.max_chunks) <= INT32_MAX - kLeast;
+    return (int64_t)s.B * s.Hkv * (kOpen + kPerChunk * (int64_t)s.max_chunks) <= INT32_MAX - kLeast;
 }
 
 size_t paged_dense_workspace(const PagedShape& s) { return sizeof(float) * part_floats(s) * 2 * kPerSm * (size_t)sm_count(); }

@@ -149,15 +149,32 @@ __device__ __forceinline__ void select(const Key* keys, int n, int k, SelectScra
         return;
     }
     if (n <= kCount) {
-        // 2^e threads count for one key, each over the keys of its own turn.
+        // 2^e threads count for one key, each over the pairs of keys of its own
+        // turn.  Upper words first; where two keys tie there, whole keys (and
+        // of equal ones the lower place wins).
         const int e = n <= 8 * Warps ? 2 : n <= 16 * Warps ? 1 : 0;
-        const int i = tid >> e;
+        const int i = tid >> e, turn = tid & ((1 << e) - 1);
         const Key x = i < n ? keys[i] : 0ull;
-        int beat = 0;
+        const uint32_t upper = uint32_t(x >> 32);
+        int beat = 0, same = 0;
 #pragma unroll 4
-        for (int j = tid & ((1 << e) - 1); j < n; j += 1 << e) {
-            const Key w = keys[j];
-            beat += w > x || (w == x && j < i);
+        for (int j = 2 * turn; j + 1 < n; j += 2 << e) {
+            const uint4 w = *reinterpret_cast<const uint4*>(keys + j);
+            beat += w.y > upper;
+            beat += w.w > upper;
+            same += w.y == upper;
+            same += w.w == upper;
+        }
+        if ((n & 1) && turn == 0) {
+            const uint32_t w = uint32_t(keys[n - 1] >> 32);
+            beat += w > upper;
+            same += w == upper;
+        }
+        if (e > 0) same += __shfl_xor_sync(0xFFFFFFFFu, same, 1);
+        if (e > 1) same += __shfl_xor_sync(0xFFFFFFFFu, same, 2);
+        if (__syncthreads_or(i < n && same > 1)) {   // (a key ties with itself)
+            beat = 0;
+            for (int j = turn; j < n; j += 1 << e) beat += keys[j] > x || (keys[j] == x && j < i);
         }
         if (e > 0) beat += __shfl_xor_sync(0xFFFFFFFFu, beat, 1);
         if (e > 1) beat += __shfl_xor_sync(0xFFFFFFFFu, beat, 2);

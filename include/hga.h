@@ -457,7 +457,7 @@ size_t hga_paged_workspace_size(const hga_paged_params* p);
  *         on the GPU need workspaces of their own.
  * At most 8 q-heads per kv-head; HGA_ERR_UNSUPPORTED too when the routing
  * state of max_chunks and k_c exceeds shared memory, or for dense attention
- * when B * Hkv * (2 * max_chunks + 1) comes near 2^31. */
+ * when B * Hkv * (2 * max_chunks + 12) exceeds 2^31. */
 int hga_paged_decode(const hga_paged_params* p, const hga_paged_cache* c, const int32_t* pos, const void* q,
                      float* O, float* lse, int32_t* cidx, int32_t* gidx, void* workspace, size_t ws_bytes,
                      hga_stream_t stream);
