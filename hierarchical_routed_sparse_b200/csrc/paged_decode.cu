@@ -25,8 +25,8 @@
 //
 // A step is a chain of about ten dependent steps (position, scores, exchange,
 // selection, group scores, exchange, selection, tiles, merge, exchange) of
-// 0.5 - 2 us each, which bounds it: 14.5 us for one sequence at 16K context
-// (8 kv-heads, d 128, k_c 8, k_g 32; 2.3 MB), 42 us for 64 (103 MB, 2.4 TB/s:
+// 0.5 - 2 us each, which bounds it: 13.7 us for one sequence at 16K context
+// (8 kv-heads, d 128, k_c 8, k_g 32; 2.3 MB), 41 us for 64 (103 MB, 2.5 TB/s:
 // at four CTAs an SM the chains wait for memory half of their time).
 #include "paged.cuh"
 #include "paged_attend.cuh"

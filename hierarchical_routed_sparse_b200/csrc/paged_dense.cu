@@ -13,8 +13,8 @@
 //
 // The kernel streams every code once; what bounds it is instruction issue, at
 // about 800 a tile (paged_attend.cuh): 8 sequences of up to 16K, 8 kv-heads
-// (156 MB) take 40.6 us with the join, 3.8 TB/s, and one of 50000 with 2
-// kv-heads (26 MB) 16 us, most of it the two kernels' chains.
+// (156 MB) take 37.9 us with the join, 4.1 TB/s, and one of 50000 with 2
+// kv-heads (26 MB) 13.8 us, most of it the two kernels' chains.
 #include "paged.cuh"
 #include "paged_attend.cuh"
 #include "sm100.cuh"
@@ -109,6 +109,25 @@ __device__ __forceinline__ void find(const Args& g, const Row& row, int tile, in
     b = g.s.B;
 }
 
+// Where a border between two CTAs goes that would be `o` tiles into a unit of
+// n: not among the open rows' tiles, which are one piece, nor a few tiles
+// before the unit's end.
+__device__ __forceinline__ int border(int o, int n)
+{
+    if (n < kOpen + kWarps) return 2 * o < n ? 0 : n;            // a short unit stays whole
+    if (o < kOpen) return 2 * o < kOpen ? 0 : kOpen;
+    return n - o < kWarps ? n : o;
+}
+
+// As find, for the border nearest to the tile; moves the tile there.
+__device__ __forceinline__ void find_border(const Args& g, const Row& row, int& tile, int& b, int& first)
+{
+    if (tile >= row.total) return;
+    find(g, row, tile, b, first);
+    const int n = tiles_of(g, b), o = (tile - first) % n;
+    tile += border(o, n) - o;
+}
+
 // (A multiple of 4 floats, as a part's rows are read.)
 __host__ __device__ inline size_t part_floats(const PagedShape& s) { return ((size_t)s.G * s.d + 2 * (size_t)s.G + 3) & ~size_t(3); }
 
@@ -128,10 +147,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) paged_dense_kernel(const __g
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = g.s.G;
     const Row row(g);
     if ((int)blockIdx.x >= row.ctas || row.total == 0) return;
-    int at = row.begin(blockIdx.x);
-    const int end = row.begin(blockIdx.x + 1);
-    int b, first;                                    // first: of the sequence's first unit
-    find(g, row, at, b, first);
+    int at = row.begin(blockIdx.x), end = row.begin(blockIdx.x + 1);
+    int b = 0, first = 0;                            // first: of the sequence's first unit
+    find_border(g, row, end, b, first);
+    find_border(g, row, at, b, first);
 
     while (at < end) {
         const int n = tiles_of(g, b);
@@ -221,10 +240,11 @@ __global__ void __launch_bounds__(kThreads, kPerSm) paged_dense_kernel(const __g
 // four elements each, kLots parts at a time.  Until pdl_wait only the caller's
 // inputs are read: the first kernel's CTAs let this one start after their own
 // wait, when whatever wrote the inputs is done.
-constexpr int kJoinThreads = 512, kParts = 256;      // parts whose factors are formed at once
-template <int D> __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ Args g)
+// Many threads where there are few units, which have many parts each.
+template <int D, int kJoinThreads> __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ Args g)
 {
     constexpr int kLots = kJoinThreads / (D / 4), kJoinWarps = kJoinThreads / 32;
+    constexpr int kParts = kJoinThreads / 2;         // parts whose factors are formed at once
     __shared__ float4 s_o[kLots][D / 4];
     __shared__ float s_f[kParts], s_red[2][kJoinWarps];
     const int tid = threadIdx.x, e = tid % (D / 4), lot = tid / (D / 4), lane = tid & 31, G = g.s.G;
@@ -236,7 +256,13 @@ template <int D> __global__ void __launch_bounds__(kJoinThreads) paged_join_kern
 #pragma unroll 4
     for (int i = lane; i < b; i += 32) before += tiles_of(g, i);
     const int n = tiles_of(g, b), unit0 = warp_sum_int(before) * g.s.Hkv + n * h;
-    const int c0 = n > 0 ? row.cta_of(unit0) : 0, c1 = n > 0 ? row.cta_of(unit0 + n - 1) : 0;
+    int c0 = 0, c1 = 0;                              // the unit's first and last CTA
+    if (n > 0) {
+        c0 = row.cta_of(unit0);
+        c1 = row.cta_of(unit0 + n - 1);
+        while (c0 + 1 < row.ctas && row.begin(c0 + 1) < unit0 + n && border(row.begin(c0 + 1) - unit0, n) == 0) ++c0;
+        while (row.begin(c1) > unit0 && border(row.begin(c1) - unit0, n) == n) --c1;
+    }
     pdl_wait();
     pdl_trigger();
     if (n == 0) {
@@ -306,7 +332,9 @@ template <typename TIn, int D, int CACHE> cudaError_t launch(const Args& g, cuda
     const size_t smem = dense_smem<D>(g.s);
     if (cudaError_t e = allow_smem(k, (int)smem)) return e;
     if (cudaError_t e = launch_pdl(k, dim3((unsigned)g.grid), dim3(kThreads), smem, st, g)) return e;
-    return launch_pdl(paged_join_kernel<D>, dim3((unsigned)(g.s.B * g.s.Hq)), dim3(kJoinThreads), 0, st, g);
+    const dim3 grid((unsigned)(g.s.B * g.s.Hq));
+    return g.s.B * g.s.Hkv < 64 ? launch_pdl(paged_join_kernel<D, 512>, grid, dim3(512), 0, st, g)
+                                : launch_pdl(paged_join_kernel<D, 128>, grid, dim3(128), 0, st, g);
 }
 
 template <typename TIn, int D> cudaError_t by_cache(const Args& g, cudaStream_t st)

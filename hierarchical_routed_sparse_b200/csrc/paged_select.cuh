@@ -11,7 +11,7 @@
 //
 // What bounds these is the length of a warp's instruction chain (a lone warp
 // issues one in about 4 cycles): 256 keys, k 8 take 1.5 us and 64 keys, k 32
-// 0.9 us; a bisection over the same 256 keys 2.5 us, and a histogram of 256
+// about 1 us, barriers included; a bisection over the same 256 keys 2.5 us, and a histogram of 256
 // bins by all threads (five barriers) 2 us.
 #pragma once
 

@@ -675,3 +675,28 @@ def test_queries_of_extreme_size(size):
     o_ref, l_ref = R.attend(q[0].double().cpu().numpy(), k, v, 1 / math.sqrt(128))
     assert np.abs(O[0] - o_ref).max() <= 2.0 ** -20 * np.abs(v).max()
     assert (np.abs(lse[0] - l_ref) <= 2.0 ** -20 * (1 + np.abs(l_ref))).all()
+
+
+@pytest.mark.parametrize("long_at", [0, 17, 39])
+def test_dense_batch_of_uneven_lengths(long_at):
+    # One long sequence, cut over most of the GPU, among short and empty ones
+    # that stay whole.
+    lens = [1 + 37 * b % 300 for b in range(40)]
+    lens[5] = lens[20] = 0
+    lens[long_at] = 20011
+    p = _params(40, 8, 2, 128, sum(n // 64 + 1 for n in lens), 313, "bf16", "int8")
+    c = _wide(p, lens)
+    q = torch.randn(40, 8, 128, device="cuda").bfloat16()
+    pos = [n - 1 for n in lens]
+    _check_decode(c, "int8", pos, q, _decode(c, pos, q, rows=False), rows=False)
+
+
+@pytest.mark.parametrize("B,Hkv,n", [(33, 3, 64), (1, 1, 65), (2, 1, 700), (7, 5, 257), (100, 2, 1), (13, 1, 4000)])
+def test_dense_borders(B, Hkv, n):
+    # Units around the sizes at which a CTA's share begins and ends in them.
+    lens = [max(1, n - 61 * (b % 5)) for b in range(B)]
+    p = _params(B, 2 * Hkv, Hkv, 64, B * (n // 64 + 1), n // 64 + 1, "fp32", "e4m3")
+    c, q = _filled(p, "e4m3", lens, clustered=False)
+    pos = [m - 1 for m in lens]
+    _check_decode(c, "e4m3", pos, q, _decode(c, pos, q, rows=False), rows=False)
+    assert hga.device_check() == 0
