@@ -23,6 +23,7 @@ import math
 
 import torch
 from torch import nn
+from torch.autograd.function import once_differentiable
 
 from . import binding as B
 
@@ -142,7 +143,10 @@ class HGAAttention(torch.autograd.Function):
 class RotaryHeads(torch.autograd.Function):
     """x [B][T][H][d] rotated by its positions pos0 + t, in the attention's
     layout [B][H][T][d] and type (hga_rope_fwd); the gradient goes back
-    through the transposed rotation (hga_rope_bwd)."""
+    through the transposed rotation (hga_rope_bwd), once: a second derivative
+    is refused, not left out.  Forward and gradient can be captured together in
+    a CUDA graph when no eager graph of the same leaves lives (as with any
+    autograd function)."""
 
     @staticmethod
     def forward(ctx, x, table, pos0: int, interleaved: bool, dtype):
@@ -156,6 +160,7 @@ class RotaryHeads(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         table, = ctx.saved_tensors
         dx = torch.empty(ctx.shape, device=dy.device, dtype=ctx.dtype)

@@ -94,3 +94,35 @@ def test_positions_past_the_table_are_refused():
     layer = HGASegmentLayer(64, 2, 1, 64, rope=hga.rope_table(100, 64))
     with pytest.raises(hga.HGAError):
         layer.segment(torch.randn(1, 128, 64, device="cuda"))
+
+
+def test_a_second_derivative_is_refused():
+    x = torch.randn(1, 8, 1, 64, device="cuda", requires_grad=True)
+    y = RotaryHeads.apply(x, hga.rope_table(8, 64), 0, False, torch.float32)
+    dx, = torch.autograd.grad((y ** 3).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        dx.sum().backward()
+
+
+def test_gradient_captured_and_replayed():
+    # Forward and gradient in one graph, replayed on other values.  (With an
+    # eager graph of the same leaf alive PyTorch's own stream bookkeeping
+    # invalidates any capture of a gradient, whatever the function.)
+    table = hga.rope_table(200, 64)
+    x = torch.randn(2, 150, 3, 64, device="cuda", requires_grad=True)
+    w = torch.randn(2, 3, 150, 64, device="cuda")
+    run = lambda: torch.autograd.grad(RotaryHeads.apply(x, table, 50, True, torch.bfloat16), x, w.bfloat16())[0]  # noqa: E731
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dx = run()
+    with torch.no_grad():
+        w.normal_()
+    dx.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(dx, run())
