@@ -225,11 +225,23 @@ __device__ __forceinline__ void load4(const float* p, float (&y)[4])
     const float4 w = __ldg(reinterpret_cast<const float4*>(p));
     y[0] = w.x; y[1] = w.y; y[2] = w.z; y[3] = w.w;
 }
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&y)[4])
+__device__ __forceinline__ void widen4(uint2 w, float (&y)[4])
 {
-    const uint2 w = __ldg(reinterpret_cast<const uint2*>(p));
     y[0] = __uint_as_float(w.x << 16); y[1] = __uint_as_float(w.x & 0xFFFF0000u);
     y[2] = __uint_as_float(w.y << 16); y[3] = __uint_as_float(w.y & 0xFFFF0000u);
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&y)[4])
+{
+    widen4(__ldg(reinterpret_cast<const uint2*>(p)), y);
+}
+__device__ __forceinline__ void load4_shared(const float* p, float (&y)[4])
+{
+    const float4 w = *reinterpret_cast<const float4*>(p);
+    y[0] = w.x; y[1] = w.y; y[2] = w.z; y[3] = w.w;
+}
+__device__ __forceinline__ void load4_shared(const __nv_bfloat16* p, float (&y)[4])
+{
+    widen4(*reinterpret_cast<const uint2*>(p), y);
 }
 
 // The references and sums of one head's parts, one part a lane of N neighbours
@@ -361,6 +373,12 @@ __device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_g
 __device__ __forceinline__ void fetch_wait()
 {
     asm volatile("cp.async.wait_group %0;" ::"n"(kHalves - 1) : "memory");
+    __syncwarp();
+}
+
+__device__ __forceinline__ void fetch_wait_all()
+{
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
 }
 
@@ -575,22 +593,96 @@ __device__ __forceinline__ void split3(float x0, float x1, uint32_t (&p)[3])
     }
 }
 
+// 16 open rows from row0 on, of which those below `rows` are there; the others
+// count as zero.  key(), value(): a 16-byte piece of the tile's row.
+template <typename TIn, int D> struct OpenGlobal {
+    const float* k;
+    const TIn* v;
+    const TIn* q;                                    // the kv-head's queries
+    int row0, rows;
+    __device__ __forceinline__ void query(int head, int e, float (&y)[4]) const { load4(q + head * D + e, y); }
+    __device__ __forceinline__ float4 key(int row, int piece) const
+    {
+        return row0 + row < rows ? __ldg(reinterpret_cast<const float4*>(k + (row0 + row) * D) + piece)
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __device__ __forceinline__ uint4 value(int row, int piece) const
+    {
+        return row0 + row < rows ? __ldg(reinterpret_cast<const uint4*>(v + (row0 + row) * D) + piece)
+                                 : make_uint4(0u, 0u, 0u, 0u);
+    }
+};
+
+// The same from a slot of shared memory that cp.async has filled (values of 4
+// bytes stay in global memory).  Pieces change places so that a quarter of a
+// warp reads eight different ones: keys by the row's parity, values by the row
+// pair.
+template <typename TIn, int D> struct OpenSlot {
+    static constexpr bool kValues = sizeof(TIn) == 2;
+    static constexpr int kKeyBytes = 16 * D * 4, kBytes = kKeyBytes + (kValues ? 16 * D * (int)sizeof(TIn) : 0);
+    static constexpr int N = D / 8 * (int)sizeof(TIn) / 16;      // pieces of a row that a lane takes
+    static constexpr int kQueryRow = D + 16;         // elements; the eight heads' pieces lie in different banks
+    const uint8_t* slot;
+    TIn* qs;                                         // the queries' place, common to the CTA's warps
+    OpenGlobal<TIn, D> rest;
+    __device__ __forceinline__ void query(int head, int e, float (&y)[4]) const { load4_shared(qs + head * kQueryRow + e, y); }
+    // By the whole warp (every warp that reads them writes all of them).
+    __device__ __forceinline__ void fetch_queries(int G, int lane) const
+    {
+        constexpr int kPieces = D * (int)sizeof(TIn) / 16, kEach = 16 / (int)sizeof(TIn);
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(qs);
+        for (int i = lane; i < G * kPieces; i += 32)
+            cp16<0, 0>(to + (i / kPieces * kQueryRow + i % kPieces * kEach) * (int)sizeof(TIn), rest.q + i * kEach, 16);
+    }
+
+    static __device__ __forceinline__ int key_at(int row, int piece) { return 16 * (row * (D / 4) + (piece ^ (4 * (row & 1)))); }
+    static __device__ __forceinline__ int value_at(int row, int piece)
+    {
+        const int p = row >> 1;
+        return kKeyBytes + 16 * (row * (D / 8) + (piece ^ (N == 1 ? 2 * (p & 3) : 4 * (p & 1) + ((p >> 1) & 1))));
+    }
+    // By the whole warp; the copies are the warp's own, not committed yet.
+    __device__ __forceinline__ void fetch(int lane) const
+    {
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(slot);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            const int row = (32 * i + lane) / (D / 4), piece = (32 * i + lane) % (D / 4);
+            const bool there = rest.row0 + row < rest.rows;
+            cp16<0, 0>(to + key_at(row, piece), rest.k + (there ? (rest.row0 + row) * D + 4 * piece : 0), there ? 16 : 0);
+        }
+        if constexpr (kValues) {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                const int row = (32 * i + lane) / (D / 8), piece = (32 * i + lane) % (D / 8);
+                const bool there = rest.row0 + row < rest.rows;
+                cp16<0, 0>(to + value_at(row, piece), rest.v + (there ? (rest.row0 + row) * D + 8 * piece : 0), there ? 16 : 0);
+            }
+        }
+    }
+    __device__ __forceinline__ float4 key(int row, int piece) const
+    {
+        return *reinterpret_cast<const float4*>(slot + key_at(row, piece));
+    }
+    __device__ __forceinline__ uint4 value(int row, int piece) const
+    {
+        if constexpr (kValues) return *reinterpret_cast<const uint4*>(slot + value_at(row, piece));
+        else return rest.value(row, piece);
+    }
+};
+
 // A lane's values of 16 open rows: rows 2t, 2t + 1 and 8 + 2t, 8 + 2t + 1,
-// d = (D/8) g .. + D/8 - 1; rows that are not there count as zero.
+// d = (D/8) g .. + D/8 - 1.
 template <typename TIn, int D> struct OpenValues {
     static constexpr int N = D / 8 * (int)sizeof(TIn) / 16;      // 16-byte pieces of a row
     uint4 w[4][N];
-    __device__ __forceinline__ void load(const TIn* v, int row0, int rows, int lane)
+    template <typename Open> __device__ __forceinline__ void load(const Open& open, int lane)
     {
         const int g = lane >> 2, t = lane & 3;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const int row = row0 + 8 * (x / 2) + 2 * t + x % 2;
+        for (int x = 0; x < 4; ++x)
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                w[x][i] = row < rows ? __ldg(reinterpret_cast<const uint4*>(v + row * D + (D / 8) * g) + i)
-                                     : make_uint4(0u, 0u, 0u, 0u);
-        }
+            for (int i = 0; i < N; ++i) w[x][i] = open.value(8 * (x / 2) + 2 * t + x % 2, N * g + i);
     }
     __device__ __forceinline__ uint32_t word(int x, int i) const
     {
@@ -621,32 +713,29 @@ template <typename TIn, int D> struct OpenValues {
     }
 };
 
-// Keys row0 .. row0 + 15 of the open rows (those below `rows`).
-template <typename TIn, int D>
-__device__ __forceinline__ void attend_open(Running<D>& run, const TIn* q, int G, const float* k, const TIn* v, int row0,
-                                            int rows, float scale, int lane)
+// One tile of open rows (OpenGlobal, OpenSlot), of which the first `rows` are there.
+template <typename TIn, int D, typename Open>
+__device__ __forceinline__ void attend_open(Running<D>& run, int G, const Open& open, int rows, float scale, int lane)
 {
     constexpr bool kF32 = sizeof(TIn) == 4;
     const int g = lane >> 2, t = lane & 3;
-    const int ra = row0 + g, rz = row0 + 8 + g;
-    const bool ha = ra < rows, hz = rz < rows;
-    const float4 none = make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool ha = g < rows, hz = 8 + g < rows;
     float s[4] = {0.f, 0.f, 0.f, 0.f}, r[4] = {0.f, 0.f, 0.f, 0.f};
     // All of the tile's loads at once, where the registers reach (a tile is one
     // round trip and a chain of a few hundred instructions).
     OpenValues<TIn, D> val;
-    if constexpr (!kF32) val.load(v, row0, rows, lane);
+    if constexpr (!kF32) val.load(open, lane);
     float4 ka[D / 16], kz[D / 16];
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
-        ka[i] = ha ? __ldg(reinterpret_cast<const float4*>(k + ra * D + 16 * i + 4 * t)) : none;
-        kz[i] = hz ? __ldg(reinterpret_cast<const float4*>(k + rz * D + 16 * i + 4 * t)) : none;
+        ka[i] = open.key(g, 4 * i + t);
+        kz[i] = open.key(8 + g, 4 * i + t);
     }
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {               // d = 16 i + 4 t .. + 3: two products of 8
         const float4 xa = ka[i], xz = kz[i];
         float y[4] = {0.f, 0.f, 0.f, 0.f};
-        if (g < G) load4(q + g * D + 16 * i + 4 * t, y);
+        if (g < G) open.query(g, 16 * i + 4 * t, y);
         uint32_t h[8], l[8];
         split_tf32(xa.x, h[0], l[0]);
         split_tf32(xz.x, h[1], l[1]);
@@ -673,7 +762,7 @@ __device__ __forceinline__ void attend_open(Running<D>& run, const TIn* q, int G
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[e] = (e < 2 ? ha : hz) ? (s[e] + r[e]) * scale : -INFINITY;
-    if constexpr (kF32) val.load(v, row0, rows, lane);
+    if constexpr (kF32) val.load(open, lane);
     const float lv = val.log2_most();
     run.follow(fmaxf(s[0], s[2]) + lv, fmaxf(s[1], s[3]) + lv);
     const float e0 = ex2(s[0] - run.R0), e1 = ex2(s[1] - run.R1), e2 = ex2(s[2] - run.R0), e3 = ex2(s[3] - run.R1);

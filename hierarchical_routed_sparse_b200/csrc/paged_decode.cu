@@ -11,7 +11,7 @@
 // kept groups' held values and the open rows 0 .. p % 64:
 //     O = softmax(scale q K^T) V,  lse = log sum exp (scale q K^T).
 //
-// A cluster of S CTAs (of 4 warps, or 6 when S > 1) takes one (batch, kv-head).
+// A cluster of S CTAs (of 4, 6 or 8 warps) takes one (batch, kv-head).
 //   * Scoring: CTA r scores the r-th part of the candidates and writes their
 //     keys into every peer's shared memory; each CTA then makes the same
 //     selection (paged_select.cuh).
@@ -26,8 +26,10 @@
 // A step is a chain of about ten dependent steps (position, scores, exchange,
 // selection, group scores, exchange, selection, tiles, merge, exchange) of
 // 0.5 - 2 us each, which bounds it: 13.7 us for one sequence at 16K context
-// (8 kv-heads, d 128, k_c 8, k_g 32; 2.3 MB), 41 us for 64 (103 MB, 2.5 TB/s:
-// at four CTAs an SM the chains wait for memory half of their time).
+// (8 kv-heads, d 128, k_c 8, k_g 32; 2.3 MB), 37.4 us for 64 (103 MB, 2.8 TB/s:
+// all score at once, then all wait for each other's loads in short chains).
+#include <algorithm>
+
 #include "paged.cuh"
 #include "paged_attend.cuh"
 #include "paged_select.cuh"
@@ -44,6 +46,19 @@ using sm100::smem_u32;
 constexpr int kMaxS = 8;                             // CTAs per (batch, kv-head); warps of one are at most as many
 constexpr int kSitePage = 421, kSiteLength = 422;
 
+// Dynamic shared memory.  The routing's keys (and the open rows, then their
+// parked outputs), the warps' rings and the warps' outputs follow one another
+// in the same place; the page table's first
+// kTable entries, the kept chunks and groups with their pages, and what peers
+// write (inbox) have places of their own.
+constexpr int kTable = 2048;
+struct Layout {
+    uint32_t ckeys, gkeys, scratch, slots, rings, merge, table, crow, cpage, grow, gpage, query, inbox;
+    int n_slots;
+    size_t total;
+};
+inline size_t up16(size_t x) { return (x + 15) & ~size_t(15); }
+
 struct Args {
     PagedShape s;
     hga_paged_cache c;
@@ -54,38 +69,60 @@ struct Args {
     int32_t* cidx;
     int32_t* gidx;
     int S;
+    Layout L;
 };
 
-// Dynamic shared memory.  The routing's keys (and the open rows' parked
-// outputs), the warps' rings and the warps' outputs follow one another in the
-// same place; the page table's first
-// kTable entries, the kept chunks and groups with their pages, and what peers
-// write (inbox) have places of their own.
-constexpr int kTable = 2048;
-struct Layout {
-    size_t ckeys, gkeys, scratch, parked, rings, merge, table, crow, cpage, grow, gpage, inbox, total;
-};
-__host__ __device__ inline size_t up16(size_t x) { return (x + 15) & ~size_t(15); }
-__host__ __device__ inline size_t larger(size_t a, size_t b) { return a > b ? a : b; }
-template <int D, int kWarps> __host__ __device__ inline Layout layout(const PagedShape& s, int S)
+// Where a CTA has an SM to itself, or half of one, open rows are read when they
+// are attended.  With more of them a load then takes microseconds, under the
+// scoring of the others, so the copies start before the scoring (64 sequences of
+// up to 16K: 41.4 us without, 37.5 with them; one: 13.7 and 15.2).
+template <int kWarps> constexpr bool kStaged = kWarps == 4;
+// The slots hold open rows, then a warp's parked outputs: one for each warp but
+// the first, and one for the fourth tile, as far as they leave room for four
+// CTAs an SM (that many bytes each, 1 KB of the system's and 1 KB of `us`
+// besides).
+constexpr size_t kRoom4 = 55 * 1024;
+constexpr int kOpenTiles = kChunk / 16;
+template <typename TIn, int D, int kWarps> __host__ __device__ constexpr size_t slot_bytes()
 {
-    Layout L;
+    static_assert(OpenSlot<TIn, D>::kBytes >= 4 * Running<D>::kParked, "a warp parks its outputs in its slot");
+    return kStaged<kWarps> ? OpenSlot<TIn, D>::kBytes : 4 * Running<D>::kParked;
+}
+template <typename TIn, int D, int kWarps> Layout layout(const PagedShape& s, int S)
+{
+    Layout L{};
     const size_t nc = s.max_chunks, wc = s.wc, wg = s.wg;
-    L.ckeys = L.rings = L.merge = 0;
-    L.gkeys = up16(L.ckeys + 8 * nc);
-    L.scratch = up16(L.gkeys + 8 * 8 * wc);
-    L.parked = up16(L.scratch + sizeof(SelectScratch<kWarps>));
-    const size_t keys = L.parked + 4 * Running<D>::kParked * (kWarps - 1);
+    const bool thin = nc > kThin || 8 * wc > kThin;
+    const size_t gkeys = up16(8 * nc), scratch = up16(gkeys + 8 * 8 * wc);
+    const size_t slots = up16(scratch + (thin ? sizeof(SelectScratch<kWarps>) : SelectScratch<kWarps>::kSmall));
+    const size_t table = up16(4 * std::min<size_t>(nc, kTable)), crow = up16(4 * wc), grow = up16(4 * wg);
+    const size_t query = kStaged<kWarps> ? up16(sizeof(TIn) * s.G * OpenSlot<TIn, D>::kQueryRow) : 0;
+    constexpr size_t slot = slot_bytes<TIn, D, kWarps>();
+    L.n_slots = std::min(kWarps - 1, (kOpenTiles + S - 1) / S);
+    if (kStaged<kWarps>) {
+        const size_t used = slots + table + 2 * crow + 2 * grow + query;
+        L.n_slots = used < kRoom4 ? (int)std::clamp<size_t>((kRoom4 - used) / slot, 1, kOpenTiles) : 1;
+    }
     const size_t rings = sizeof(Half<D>) * kHalves * kWarps, merge = 4 * (size_t)kWarps * s.G * (D + 3);
-    L.table = up16(larger(keys, larger(rings, merge)));
-    L.crow = L.table + 4 * (nc < kTable ? nc : kTable);
-    L.cpage = L.crow + 4 * wc;
-    L.grow = L.cpage + 4 * wc;
-    L.gpage = L.grow + 4 * wg;
-    L.inbox = up16(L.gpage + 4 * wg);
+    size_t at = up16(std::max({slots + slot * L.n_slots, rings, merge}));
+    auto take = [&](size_t n) {
+        const size_t from = at;
+        at += up16(n);
+        return (uint32_t)from;                       // (a total that is too large is refused)
+    };
+    L.gkeys = (uint32_t)gkeys;
+    L.scratch = (uint32_t)scratch;
+    L.slots = (uint32_t)slots;
+    L.table = take(table);
+    L.crow = take(crow);
+    L.cpage = take(crow);
+    L.grow = take(grow);
+    L.gpage = take(grow);
+    L.query = take(query);
     // From each peer: d / S elements of its outputs, its G references and sums
     // (and a factor for each of them).
-    L.total = up16(L.inbox + (S > 1 ? 4 * ((size_t)s.G * D + 3 * (size_t)s.G * S) : 0));
+    L.inbox = take(S > 1 ? 4 * ((size_t)s.G * D + 3 * (size_t)s.G * S) : 0);
+    L.total = at;
     return L;
 }
 
@@ -180,8 +217,10 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 4 ? 4 : 2) paged_decode
     const int S = g.S, rank = S > 1 ? (int)cluster_rank() : 0;
     const int64_t bh = blockIdx.x / S;
     const int b = int(bh / g.s.Hkv), h = int(bh % g.s.Hkv), G = g.s.G;
-    const Layout L = layout<D, kWarps>(g.s, S);
+    const Layout& L = g.L;
     if (S > 1) cluster_arrive();                     // waited for before the first write to a peer
+    // The arguments come into the constant cache while the kernel before ends.
+    asm volatile("" ::"r"(L.gkeys), "r"(L.inbox), "r"(L.n_slots), "r"(g.s.wg), "l"(g.c.k_pages), "l"(g.c.table), "l"(g.gidx));
     pdl_wait();
     pdl_trigger();
 
@@ -216,6 +255,25 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 4 ? 4 : 2) paged_decode
         return;
     }
     const int c0 = int(p / kChunk), rows = int(p % kChunk) + 1;
+    // The open rows, 16 at a time, go to the warps but the first (as many as have
+    // slots), tile i to CTA S - 1 - i mod S.
+    const int workers = min(L.n_slots, kWarps - 1);
+    const int turn = S - 1 - rank + S * (warp - 1), turns = S * workers, tiles = (rows + 15) / 16;
+    const bool own_tile = warp > 0 && warp <= workers && turn < tiles, spare = L.n_slots == kWarps;
+    uint8_t* const slot = sm + L.slots + slot_bytes<TIn, D, kWarps>() * (warp - 1);
+    auto rows_at = [&](int i) {
+        const int64_t row0 = bh * kChunk * D;
+        return OpenGlobal<TIn, D>{g.c.k_tail + row0, static_cast<const TIn*>(g.c.v_tail) + row0, q, 16 * i, rows};
+    };
+    auto slot_of = [&](int i) {
+        return OpenSlot<TIn, D>{i == turn || !spare ? slot : sm + L.slots + slot_bytes<TIn, D, kWarps>() * (kWarps - 1),
+                                reinterpret_cast<TIn*>(sm + L.query), rows_at(i)};
+    };
+    if (kStaged<kWarps> && own_tile) {
+        slot_of(turn).fetch_queries(G, lane);
+        for (int i = turn; i < tiles && (i == turn || spare); i += turns) slot_of(i).fetch(lane);
+        fetch_commit();
+    }
     auto page_of = [&](int c) {
         return (int32_t)page_or_none(c < kTable ? tab[c] : __ldg(table + c), g.s.n_pages, kSitePage);
     };
@@ -244,18 +302,28 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 4 ? 4 : 2) paged_decode
             cluster_arrive();                    // for the groups' push
         }
     }
-    // The open rows, 16 at a time, while the first warp selects (up to 512
-    // chunks are its work alone): tile i to CTA S - 1 - i mod S.
-    float* parked = reinterpret_cast<float*>(sm + L.parked) + Running<D>::kParked * (warp - 1);
-    const int turn = S - 1 - rank + S * (warp - 1), tiles = (rows + 15) / 16;
-    const bool own_tile = turn < tiles;
-    if (warp > 0 && own_tile) {
+    // The open rows are attended while the first warp selects (up to 512 chunks
+    // are its work alone).
+    float* const parked = reinterpret_cast<float*>(slot);
+    if (own_tile) {
         Running<D> run;
         run.init();
-        const int64_t row0 = bh * kChunk * D;
-        for (int i = turn; i < tiles; i += S * (kWarps - 1))
-            attend_open<TIn, D>(run, q, G, g.c.k_tail + row0, static_cast<const TIn*>(g.c.v_tail) + row0, 16 * i, rows,
-                                g.s.scale * kLog2e, lane);
+        if constexpr (kStaged<kWarps>) {
+            fetch_wait_all();
+#pragma unroll 1
+            for (int i = turn; i < tiles; i += turns) {
+                const auto open = slot_of(i);
+                if (i != turn && !spare) {
+                    open.fetch(lane);
+                    fetch_commit();
+                    fetch_wait_all();
+                }
+                attend_open<TIn, D>(run, G, open, rows - 16 * i, g.s.scale * kLog2e, lane);
+                __syncwarp();
+            }
+        } else {                                     // one tile at most: the cluster has four slots or more
+            attend_open<TIn, D>(run, G, rows_at(turn), rows - 16 * turn, g.s.scale * kLog2e, lane);
+        }
         run.park(parked, lane);
     }
     select<kWarps>(ckeys, c0, kc, scratch, tid, crow);
@@ -298,7 +366,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 4 ? 4 : 2) paged_decode
     const int wid = warp * S + rank, n_workers = S * kWarps;     // neighbouring tiles on different SMs
     Running<D> run;
     run.init();
-    if (warp > 0 && own_tile) run.unpark(parked, lane);
+    if (own_tile) run.unpark(parked, lane);
     __syncthreads();                                 // the rings may be filled
     {
         const int n_tiles = (ng + kTileGroups - 1) / kTileGroups;
@@ -376,24 +444,39 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 4 ? 4 : 2) paged_decode
     }
 }
 
-// CTAs per (batch, kv-head), a power of two.  Measured at 16K context, k_c 8,
-// k_g 32 (us a call with 1, 2, 4, 8 CTAs): 8 units 21.4, 16.2, 15.3, 14.5; 32
-// units 21.7, 16.3, 15.0, 16.1; 64 units 21.8, 16.4, 17.1, 32.2; 128 units
-// 25.9, 21.0, 36.7; 256 units 35.3, 42.3; 512 units 42.3, 82.1.  At 128K (k_c
-// 16, k_g 64) 32 units take 98, 44, 31, 29.  So: as many as leave a CTA an SM
-// to itself, two CTAs an SM for the first doubling and where there are many
-// chunks to score, and no more than there are chunks to share.
-int split(const PagedShape& s)
+// CTAs per (batch, kv-head), a power of two, and warps of one.  Measured, k_c 8,
+// k_g 32, d 128, us a call ("4 x 6": four CTAs of 6 warps):
+//   16K, units    8: 1 x 8 15.7, 8 x 6 14.1, 8 x 8 14.5
+//                32: 1 x 8 16.0, 2 x 6 16.0, 4 x 6 14.2, 8 x 6 15.1
+//                64: 1 x 4 20.8, 1 x 8 16.1, 2 x 6 16.1, 4 x 6 15.9
+//               128: 1 x 4 22.6, 1 x 6 19.2, 1 x 8 17.7, 2 x 6 19.8
+//               256: 1 x 4 29.7, 1 x 6 25.4, 1 x 8 26.1, 2 x 6 41.4
+//               320: 1 x 4 34.1, 1 x 6 39.7;  512: 37.4, 46.7
+//   2K,         256: 1 x 4 19.6, 1 x 6 18.8, 1 x 8 20.6
+//   128K, units  32: 1 x 8 48.5, 2 x 8 33.2, 4 x 6 27.4, 4 x 8 24.6, 8 x 8 24.5
+//  (k_c 16,      64: 1 x 8 63.8, 2 x 8 43.8, 4 x 6 38.0, 4 x 8 37.0
+//   k_g 64)     128: 1 x 8 68.0, 2 x 6 57.8, 2 x 8 52.9;  256: 1 x 6 87.7, 1 x 8 80.3
+// So: clusters as long as a CTA has an SM to itself, of 6 warps (the exchange and
+// the merge grow with the warps); then 8 warps, 6 when two CTAs share an SM, and
+// 4 when four do.  Where there are many chunks to score, 8 warps and clusters
+// for two CTAs an SM.
+struct Split {
+    int S, warps;
+};
+Split split(const PagedShape& s)
 {
     const int64_t units = (int64_t)s.B * s.Hkv, sms = sm_count();
+    if (units > 2 * sms) return {1, 4};
+    const bool many = s.max_chunks >= 1024;
     int S = 1;
-    while (S < kMaxS && S * 4 <= s.max_chunks && units * S * 2 <= (S == 1 || s.max_chunks >= 1024 ? 2 : 1) * sms) S *= 2;
-    return S;
+    while (S < kMaxS && S * 4 <= s.max_chunks && units * S * 2 <= (many ? 2 * sms : sms)) S *= 2;
+    return {S, many || (S == 1 && units <= sms) ? 8 : 6};
 }
 
-template <typename TIn, int D, int CACHE, int kWarps> cudaError_t launch(const Args& g, cudaStream_t st)
+template <typename TIn, int D, int CACHE, int kWarps> cudaError_t launch(Args g, cudaStream_t st)
 {
-    const size_t smem = layout<D, kWarps>(g.s, g.S).total;
+    g.L = layout<TIn, D, kWarps>(g.s, g.S);
+    const size_t smem = g.L.total;
     auto k = paged_decode_kernel<TIn, D, CACHE, kWarps>;
     if (cudaError_t e = allow_smem(k, (int)smem)) return e;
     cudaLaunchConfig_t cfg = {};
@@ -413,23 +496,35 @@ template <typename TIn, int D, int CACHE, int kWarps> cudaError_t launch(const A
     return cudaLaunchKernelEx(&cfg, k, g);
 }
 
-template <typename TIn, int D> cudaError_t by_cache(const Args& g, cudaStream_t st)
+template <typename TIn, int D, int CACHE> cudaError_t by_warps(const Args& g, int warps, cudaStream_t st)
 {
-    if (g.s.cache_dtype == HGA_INT8)
-        return g.S > 1 ? launch<TIn, D, HGA_INT8, 6>(g, st) : launch<TIn, D, HGA_INT8, 4>(g, st);
-    return g.S > 1 ? launch<TIn, D, HGA_E4M3, 6>(g, st) : launch<TIn, D, HGA_E4M3, 4>(g, st);
+    return warps == 8   ? launch<TIn, D, CACHE, 8>(g, st)
+           : warps == 6 ? launch<TIn, D, CACHE, 6>(g, st)
+                        : launch<TIn, D, CACHE, 4>(g, st);
+}
+
+template <typename TIn, int D> cudaError_t by_cache(const Args& g, int warps, cudaStream_t st)
+{
+    return g.s.cache_dtype == HGA_INT8 ? by_warps<TIn, D, HGA_INT8>(g, warps, st) : by_warps<TIn, D, HGA_E4M3>(g, warps, st);
 }
 
 }  // namespace
 
-size_t paged_routed_smem(const PagedShape& s) { return layout<128, 6>(s, kMaxS).total + 2048; }
+// (bfloat16 rows take the larger slots.)
+size_t paged_routed_smem(const PagedShape& s)
+{
+    return std::max({layout<__nv_bfloat16, 128, 4>(s, 1).total, layout<float, 128, 8>(s, 1).total,
+                     layout<float, 128, 8>(s, kMaxS).total}) + 2048;
+}
 
 cudaError_t launch_paged_routed(const PagedShape& s, const hga_paged_cache& c, const int32_t* pos, const void* q,
                                 float* O, float* lse, int32_t* cidx, int32_t* gidx, cudaStream_t st)
 {
-    const Args g{s, c, pos, q, O, lse, cidx, gidx, split(s)};
-    if (s.dtype == HGA_BF16) return s.d == 128 ? by_cache<__nv_bfloat16, 128>(g, st) : by_cache<__nv_bfloat16, 64>(g, st);
-    return s.d == 128 ? by_cache<float, 128>(g, st) : by_cache<float, 64>(g, st);
+    const Split x = split(s);
+    const Args g{s, c, pos, q, O, lse, cidx, gidx, x.S, {}};
+    if (s.dtype == HGA_BF16)
+        return s.d == 128 ? by_cache<__nv_bfloat16, 128>(g, x.warps, st) : by_cache<__nv_bfloat16, 64>(g, x.warps, st);
+    return s.d == 128 ? by_cache<float, 128>(g, x.warps, st) : by_cache<float, 64>(g, x.warps, st);
 }
 
 HGA_CHECK_WORD_READER(check_word_paged_routed)

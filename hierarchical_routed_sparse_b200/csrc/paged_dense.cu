@@ -192,8 +192,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) paged_dense_kernel(const __g
             const int rows = int(g.pos[b] % kChunk) + 1;
             const int64_t r0 = bh * kChunk * D;
             if (16 * warp < rows)
-                attend_open<TIn, D>(run, q, G, g.c.k_tail + r0, static_cast<const TIn*>(g.c.v_tail) + r0, 16 * warp, rows,
-                                    g.s.scale * kLog2e, lane);
+                attend_open<TIn, D>(run, G,
+                                    OpenGlobal<TIn, D>{g.c.k_tail + r0, static_cast<const TIn*>(g.c.v_tail) + r0, q,
+                                                       16 * warp, rows},
+                                    rows - 16 * warp, g.s.scale * kLog2e, lane);
         }
         held.attend(run, q, G, g.s.scale * kLog2e);
 

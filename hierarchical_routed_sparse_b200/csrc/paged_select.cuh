@@ -34,10 +34,12 @@ __device__ __forceinline__ Key ordered(double x)
 constexpr int kThin = 512;                           // keys that one warp takes at once
 constexpr int kCount = 128;                          // keys that are ranked by counting
 
+// (ids and keys are for more than kThin keys only.)
 template <int Warps> struct SelectScratch {
-    Key keys[kThin];
     uint32_t room[Warps][32];
-    int32_t ids[kThin], place[Warps][32], count[Warps];
+    int32_t place[Warps][32], count[(Warps + 3) / 4 * 4], ids[kThin];
+    Key keys[kThin];
+    static constexpr size_t kSmall = 4 * (64 * Warps + (Warps + 3) / 4 * 4);     // bytes before ids
 };
 
 // How many lanes below have their bit.

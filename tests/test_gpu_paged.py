@@ -700,3 +700,31 @@ def test_dense_borders(B, Hkv, n):
     pos = [m - 1 for m in lens]
     _check_decode(c, "e4m3", pos, q, _decode(c, pos, q, rows=False), rows=False)
     assert hga.device_check() == 0
+
+
+@pytest.mark.parametrize("d,dtype,kind", [(128, "bf16", "int8"), (64, "fp32", "e4m3"), (128, "fp32", "int8"), (64, "bf16", "e4m3")])
+@pytest.mark.parametrize("B,Hkv,width", [(100, 3, 6), (100, 3, 250), (100, 3, 900), (100, 3, 1100), (100, 3, 2100),  # four CTAs an SM
+                                         (50, 4, 250), (50, 4, 1100),                         # two
+                                         (25, 4, 250), (25, 4, 1100), (6, 8, 1100)])          # one, clusters
+def test_every_split(B, Hkv, width, d, dtype, kind):
+    # The warps and CTAs that a unit gets and the room for open rows follow from
+    # the number of units and the table's width; lengths of every count of open tiles.
+    lens = [(1 + 37 * b) % 330 for b in range(B)]
+    lens[3] = 0
+    lens[B - 1] = 320
+    G = 1 + (width + B) % 8
+    p = _params(B, Hkv * G, Hkv, d, sum(n // 64 + 1 for n in lens), width, dtype, kind, 3, 11)
+    c, q = _short_tables(p, kind, lens)
+    pos = [n - 1 for n in lens]
+    _check_decode(c, kind, pos, q, _decode(c, pos, q))
+    assert hga.device_check() == 0
+
+
+def _short_tables(p, kind, lens):
+    """A filled cache whose tables are far wider than the sequences are long."""
+    narrow = _params(p.B, p.Hq, p.Hkv, p.d, p.B * 6, 6, "bf16" if p.dtype == hga.HGA_BF16 else "fp32", kind, 3, 11)
+    made, q = _filled(narrow, kind, lens)
+    c = hga.PagedCache(hga.PagedParams(p.B, p.Hq, p.Hkv, p.d, p.B * 6, p.max_chunks, p.k_c, p.k_g, p.dtype, p.cache_dtype),
+                       **{n: getattr(made, n) for n in TENSORS})
+    c.table[:, :min(6, p.max_chunks)] = made.table[:, :min(6, p.max_chunks)]
+    return c, q
