@@ -25,7 +25,7 @@
 //
 // A step is a chain of about ten dependent steps (position, scores, exchange,
 // selection, group scores, exchange, selection, tiles, merge, exchange) of
-// 0.5 - 2 us each, which bounds it: 13.7 us for one sequence at 16K context
+// 0.5 - 2 us each, which bounds it: 13.5 us for one sequence at 16K context
 // (8 kv-heads, d 128, k_c 8, k_g 32; 2.3 MB), 37.4 us for 64 (103 MB, 2.8 TB/s:
 // all score at once, then all wait for each other's loads in short chains).
 #include <algorithm>

@@ -81,7 +81,8 @@ static __device__ __noinline__ void bisect_select(const Key* keys, int n, int k,
 
 // One warp: as bisect_select, for n <= 32 M and k <= 32; false (and nothing
 // written that counts) where it does not apply.  Works on the keys' upper
-// words: enough unless two of the few candidates tie there.
+// words, and on whole keys where two of the few candidates tie there (one
+// selection in a thousand; by bisection that one took 14 us instead of 4).
 template <int M>
 __device__ __forceinline__ bool warp_try(const Key* keys, int n, int k, int lane, uint32_t* room, int32_t* place, int32_t* out)
 {
@@ -121,7 +122,15 @@ __device__ __forceinline__ bool warp_try(const Key* keys, int n, int k, int lane
         beat += w > x;
         tie = tie || w == x;
     }
-    if (__any_sync(0xFFFFFFFFu, tie && lane < got)) return false;
+    if (__any_sync(0xFFFFFFFFu, tie && lane < got)) {            // whole keys, of equal ones the lower place
+        const Key whole = lane < got ? keys[place[lane]] : 0ull;
+        beat = 0;
+#pragma unroll 1
+        for (int o = 1; o < 32; ++o) {
+            const Key w = __shfl_sync(0xFFFFFFFFu, whole, lane + o);
+            beat += w > whole || (w == whole && ((lane + o) & 31) < lane);
+        }
+    }
     const bool keep = lane < got && beat < k;
     const unsigned kept = __ballot_sync(0xFFFFFFFFu, keep);
     if (keep) out[below(kept, lane)] = place[lane];

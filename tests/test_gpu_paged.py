@@ -728,3 +728,25 @@ def _short_tables(p, kind, lens):
                        **{n: getattr(made, n) for n in TENSORS})
     c.table[:, :min(6, p.max_chunks)] = made.table[:, :min(6, p.max_chunks)]
     return c, q
+
+
+@pytest.mark.parametrize("n_chunks,k_c,k_g", [(100, 8, 13), (200, 8, 20), (400, 8, 32), (400, 20, 32), (700, 8, 32), (700, 30, 40)])
+@pytest.mark.parametrize("near", [2, 11, 25])
+def test_scores_that_differ_in_their_last_bits(n_chunks, k_c, k_g, near):
+    # The highest scores are 1 + j 2^-40 (two of each j): float64 tells them
+    # apart, its first 32 bits do not.
+    p = _params(1, 1, 1, 64, n_chunks + 1, n_chunks + 1, "fp32", "int8", k_c, k_g)
+    lens = [64 * n_chunks + 7]
+    c = _wide(p, lens)
+    g = torch.Generator().manual_seed(near)
+    pages = c.table[0, :n_chunks].long()
+    for t, n in ((c.csum, n_chunks), (c.gsum, 8 * n_chunks)):
+        s = torch.zeros(n, 64)
+        s[:, 0] = torch.rand(n, generator=g) * 0.9
+        top = torch.randperm(n, generator=g)[:near]
+        s[top, 0] = 1.0
+        s[top, 1] = torch.arange(near).div(2, rounding_mode="floor").float() * 2.0 ** -40
+        t[pages] = s.view(n_chunks, *t.shape[1:]).cuda()
+    q = torch.zeros(1, 1, 64, device="cuda")
+    q[..., :2] = 1.0
+    _check_decode(c, "int8", [lens[0] - 1], q, _decode(c, [lens[0] - 1], q))
