@@ -75,7 +75,8 @@ struct Args {
 // Where a CTA has an SM to itself, or half of one, open rows are read when they
 // are attended.  With more of them a load then takes microseconds, under the
 // scoring of the others, so the copies start before the scoring (64 sequences of
-// up to 16K: 41.4 us without, 37.5 with them; one: 13.7 and 15.2).
+// up to 16K: 41.4 us without, 37.5 with them; 32, two CTAs an SM: 25.6 and 26.0;
+// one: 13.7 and 15.2).
 template <int kWarps> constexpr bool kStaged = kWarps == 4;
 // The slots hold open rows, then a warp's parked outputs: one for each warp but
 // the first, and one for the fourth tile, as far as they leave room for four
