@@ -32,14 +32,20 @@
 // Sums are float32.
 //
 // Running softmax, in units of log2.  With s the score and v the group's value
-// scale, a weight enters the products as e v, e = 2^(s - R).  The reference R
-// follows a tile's largest s + log2 of its largest v, so that e v stays below
-// 2^15 whatever the scales are, and it moves only when that would be exceeded:
-// R is 12 below the maximum it was set from, so most tiles find it as it
-// should be and weights down to 2^-24 of the largest keep all their bits.
-// (Open rows take the largest of their values for v, for the reference alone.)
-// The normalising sum collects e, which stays below 2^105 since log2 v counts
-// as at least -90 there; values below 2^-90 lose bits.
+// scale, the normalising sum collects e = 2^(s - R), and a weight enters the
+// products as e (v 2^-W): R is a score that has been met, W a whole number.
+// They are two numbers, not their sum, because a score can be so large that
+// a float32 next to it cannot say how large the values are, and because the
+// sum of all e must not depend on the values' size (one tile of zeros
+// beside one of 2^40).
+// Both move when a tile's largest e max(v 2^-W, 1) is above 2^15, so e stays
+// below that and so does e v 2^-W, which float16 has to hold.  W is
+// then 12 below the largest s - R + log2 v so far, so most tiles find both as
+// they should be and weights down to 2^-24 of the largest keep all their bits,
+// whatever the values' sizes.  (Open rows take the largest of their values for
+// v, for W alone.)  log2 v counts as at least -90; values below 2^-90 lose
+// bits.  Parts of a head (warps, CTAs) leave the registers as finished
+// means with their R and sum, so W stays inside.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -53,7 +59,11 @@ namespace paged {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kFloor = -1e30f;                     // R of a warp that has met no key
-constexpr float kBelow = 12.f, kAbove = 15.f;
+constexpr float kBelow = 12.f, kAbove = 32768.f;      // of W in log2; of a weight
+constexpr int kLeastV = -90;                         // log2 of the smallest values that W follows
+// Keys further below R than this count as if they were there, so that v 2^-W
+// stays a float32 however large the values of such keys are.
+constexpr float kFar = -64.f, kFarWeight = 1.f / 18446744073709551616.f;
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -136,12 +146,34 @@ template <> struct Codes<HGA_E4M3> {
     }
 };
 
+// 1 / x, off by 2^-23 of it.
+__device__ __forceinline__ float rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// log2 of a positive value rounded up (or one more): at least kLeastV; 0 where
+// the value is not finite.
+__device__ __forceinline__ int log2_above(float v)
+{
+    const int e = int(__float_as_uint(v) >> 23) - 126;
+    return e > 128 ? 0 : max(e, kLeastV);
+}
+
 // Running state of a warp: references and sums of heads 2t, 2t + 1 (the sum
-// over this lane's rows only) and their outputs.
+// over this lane's rows only), their outputs, and 2^-W of both as bfloat16
+// halves of a word (a register less than two floats, where the 128-register
+// kernels spill).
 template <int D> struct Running {
     static constexpr int kM = D / 16;
     float acc[kM][4];                                // [i]: d = (D/8) g + 2i, head 2t, 2t + 1; then d + 1
     float R0, R1, l0, l1;
+    uint32_t down;                                   // head 2t in the upper half
+
+    __device__ __forceinline__ float down0() const { return __uint_as_float(down & 0xFFFF0000u); }
+    __device__ __forceinline__ float down1() const { return __uint_as_float(down << 16); }
 
     __device__ __forceinline__ void init()
     {
@@ -151,22 +183,36 @@ template <int D> struct Running {
             for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
         R0 = R1 = kFloor;
         l0 = l1 = 0.f;
+        down = 0x00010001u * (uint32_t)((127 + 12 - kLeastV) << 7);
+        static_assert(kBelow == 12.f, "W starts at its least");
     }
-    // Move the references up where a tile's largest s + log2 v asks for it.
-    __device__ __forceinline__ void follow(float m0, float m1)
+    // R and W of one head from a tile's largest score m and log2 v; returns the
+    // factor for the outputs, and 2^-W in place of c.  W stays in [-102, 116].
+    __device__ __forceinline__ static float move(float& R, float& l, float& c, float m, float lv)
     {
-        if (!__any_sync(0xFFFFFFFFu, m0 > R0 + kAbove || m1 > R1 + kAbove)) return;
+        const float n = fmaxf(R, m), fall = R - n, W = float(127 - int(__float_as_uint(c) >> 23));
+        const float w = ceilf(fmaxf(W + fall, fmaxf(m - n, kFar) + (lv - kBelow)));
+        c = __uint_as_float(uint32_t(127 - int(w)) << 23);
+        l *= ex2(fall);
+        R = n;
+        return ex2(fall + (W - w));
+    }
+    // Move them where a tile's largest scores of this lane and its largest v
+    // ask for it.
+    __device__ __forceinline__ void follow(float m0, float m1, float v)
+    {
+        float c0 = down0(), c1 = down1();
+        const float x0 = fmaxf(ex2(m0 - R0), kFarWeight) * fmaxf(v * c0, 1.f);
+        const float x1 = fmaxf(ex2(m1 - R1), kFarWeight) * fmaxf(v * c1, 1.f);
+        if (!__any_sync(0xFFFFFFFFu, x0 > kAbove || x1 > kAbove)) return;
+        const float lv = (float)log2_above(v);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
             m0 = fmaxf(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, o));
             m1 = fmaxf(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, o));
         }
-        const float n0 = fmaxf(R0, m0 - kBelow), n1 = fmaxf(R1, m1 - kBelow);
-        const float f0 = ex2(R0 - n0), f1 = ex2(R1 - n1);
-        R0 = n0;
-        R1 = n1;
-        l0 *= f0;
-        l1 *= f1;
+        const float f0 = move(R0, l0, c0, m0, lv), f1 = move(R1, l1, c1, m1, lv);
+        down = __float_as_uint(c0) | __float_as_uint(c1) >> 16;
 #pragma unroll
         for (int i = 0; i < kM; ++i) {
             acc[i][0] *= f0;
@@ -176,7 +222,7 @@ template <int D> struct Running {
         }
     }
     // Out of the registers into shared memory (kParked floats), and back.
-    static constexpr int kParked = 32 * (4 * kM + 4);
+    static constexpr int kParked = 32 * (4 * kM + 5);
     __device__ __forceinline__ void park(float* p, int lane) const
     {
 #pragma unroll
@@ -186,6 +232,7 @@ template <int D> struct Running {
         p[32] = R1;
         p[64] = l0;
         p[96] = l1;
+        p[128] = __uint_as_float(down);
     }
     __device__ __forceinline__ void unpark(const float* p, int lane)
     {
@@ -196,8 +243,9 @@ template <int D> struct Running {
         R1 = p[32];
         l0 = p[64];
         l1 = p[96];
+        down = __float_as_uint(p[128]);
     }
-    // o [G][D], r [G], l [G] of this warp.
+    // Means o [G][D] (zeros where no key was met), r [G], l [G] of this warp.
     __device__ __forceinline__ void store(float* o, float* r, float* l, int G, int lane)
     {
         const int g = lane >> 2, t = lane & 3;
@@ -209,12 +257,15 @@ template <int D> struct Running {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             if (2 * t + e >= G) continue;
+            const float l_ = e ? l1 : l0, inv = l_ == 0.f ? 0.f : rcp(l_);
+            const float up = __uint_as_float(0x7F000000u - __float_as_uint(e ? down1() : down0()));
             float* row = o + (2 * t + e) * D + (D / 8) * g;
 #pragma unroll
-            for (int i = 0; i < kM; ++i) *reinterpret_cast<float2*>(row + 2 * i) = make_float2(acc[i][e], acc[i][2 + e]);
+            for (int i = 0; i < kM; ++i)
+                *reinterpret_cast<float2*>(row + 2 * i) = make_float2(acc[i][e] * inv * up, acc[i][2 + e] * inv * up);
             if (g == 0) {
                 r[2 * t + e] = e ? R1 : R0;
-                l[2 * t + e] = e ? l1 : l0;
+                l[2 * t + e] = l_;
             }
         }
     }
@@ -246,18 +297,20 @@ __device__ __forceinline__ void load4_shared(const __nv_bfloat16* p, float (&y)[
 
 // The references and sums of one head's parts, one part a lane of N neighbours
 // (a power of two): r becomes the common reference, l the sum for it; returns
-// the part's factor.  The whole warp takes part.
-template <int N> __device__ __forceinline__ float join_parts(float& r, float& l)
+// the part's share of that sum.  A sum of zero (no part has met a key) has
+// shares of zero, or of NaN when these were the last parts: all scores were
+// below float32.  The whole warp takes part.
+template <int N> __device__ __forceinline__ float join_parts(float& r, float& l, bool last)
 {
     float M = r;
 #pragma unroll
     for (int o = 1; o < N; o <<= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-    const float f = ex2(r - M);
-    l *= f;
+    const float mine = l * ex2(r - M);
+    l = mine;
 #pragma unroll
     for (int o = 1; o < N; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
     r = M;
-    return f;
+    return l == 0.f && !last ? 0.f : mine * rcp(l);
 }
 
 // The query as the products' B operand, and what turns a product into a
@@ -382,14 +435,6 @@ __device__ __forceinline__ void fetch_wait_all()
     __syncwarp();
 }
 
-// log2 of a positive value rounded up (or one more), for the reference only:
-// kept in [-90, 100]; 0 where the value is not finite.
-__device__ __forceinline__ float log2_above(float v)
-{
-    const int e = int(__float_as_uint(v) >> 23) - 126;
-    return e > 128 ? 0.f : (float)min(max(e, -90), 100);
-}
-
 // Scores of a tile in log2 units: s[x][0..1] of row g of group 2x for heads 2t,
 // 2t + 1, s[x][2..3] of group 2x + 1.
 template <typename TIn, int D, int CACHE>
@@ -435,16 +480,17 @@ __device__ __forceinline__ void held_outputs(Running<D>& run, const float (&s)[2
     const float4 scales = *reinterpret_cast<const float4*>(v.scale);
     const float vs[4] = {scales.x, scales.y, scales.z, scales.w};
     // (fmaxf passes a NaN scale over.)
-    const float lv = log2_above(fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3])));
-    run.follow(fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2])) + lv,
-               fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3])) + lv);
+    run.follow(fmaxf(fmaxf(s[0][0], s[0][2]), fmaxf(s[1][0], s[1][2])),
+               fmaxf(fmaxf(s[0][1], s[0][3]), fmaxf(s[1][1], s[1][3])),
+               fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3])));
+    const float w0 = run.down0(), w1 = run.down1();
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int y = 0; y < 4; ++y) {
         const float e0 = ex2(s[y / 2][2 * (y % 2)] - run.R0), e1 = ex2(s[y / 2][2 * (y % 2) + 1] - run.R1);
         run.l0 += e0;
         run.l1 += e1;
-        split_half2(e0 * vs[y], e1 * vs[y], hi[y], lo[y]);
+        split_half2(e0 * (vs[y] * w0), e1 * (vs[y] * w1), hi[y], lo[y]);
         hi[y] = transpose8(hi[y]);
         lo[y] = transpose8(lo[y]);
     }
@@ -689,8 +735,8 @@ template <typename TIn, int D> struct OpenValues {
         const uint4 q = w[x][i / 4];
         return i % 4 == 0 ? q.x : i % 4 == 1 ? q.y : i % 4 == 2 ? q.z : q.w;
     }
-    // log2_above of the tile's largest value.
-    __device__ __forceinline__ float log2_most() const
+    // The tile's largest value.
+    __device__ __forceinline__ float most() const
     {
         float top = 0.f;
         if constexpr (sizeof(TIn) == 2) {
@@ -709,7 +755,7 @@ template <typename TIn, int D> struct OpenValues {
 #pragma unroll
                 for (int i = 0; i < 4 * N; ++i) top = fmaxf(top, fabsf(__uint_as_float(word(x, i))));
         }
-        return log2_above(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top))));
+        return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top)));
     }
 };
 
@@ -763,14 +809,14 @@ __device__ __forceinline__ void attend_open(Running<D>& run, int G, const Open& 
 #pragma unroll
     for (int e = 0; e < 4; ++e) s[e] = (e < 2 ? ha : hz) ? (s[e] + r[e]) * scale : -INFINITY;
     if constexpr (kF32) val.load(open, lane);
-    const float lv = val.log2_most();
-    run.follow(fmaxf(s[0], s[2]) + lv, fmaxf(s[1], s[3]) + lv);
+    run.follow(fmaxf(s[0], s[2]), fmaxf(s[1], s[3]), val.most());
     const float e0 = ex2(s[0] - run.R0), e1 = ex2(s[1] - run.R1), e2 = ex2(s[2] - run.R0), e3 = ex2(s[3] - run.R1);
     run.l0 += e0 + e2;
     run.l1 += e1 + e3;
+    const float c0 = run.down0(), c1 = run.down1();
     uint32_t w0[3], w1[3];
-    split3(e0, e1, w0);
-    split3(e2, e3, w1);
+    split3(e0 * c0, e1 * c1, w0);
+    split3(e2 * c0, e3 * c1, w1);
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
         w0[i] = transpose8(w0[i]);

@@ -18,10 +18,9 @@
 //   * Attention: a warp takes tiles of four groups (32 keys), tile i going to
 //     warp i modulo the cluster's warps, through its own ring of asynchronous
 //     copies into mma.sync fragments (paged_attend.cuh).
-//   * Merge: every warp has a running reference, sum and unnormalised output
-//     for each head; a CTA's meet in shared memory, and each CTA
-//     combines d / S elements of every head's output (distributed shared
-//     memory).
+//   * Merge: every warp has a reference, a sum and a mean for each head; a
+//     CTA's meet in shared memory, and each CTA combines d / S elements of
+//     every head's output (distributed shared memory).
 //
 // A step is a chain of about ten dependent steps (position, scores, exchange,
 // selection, group scores, exchange, selection, tiles, merge, exchange) of
@@ -121,7 +120,7 @@ template <typename TIn, int D, int kWarps> Layout layout(const PagedShape& s, in
     L.gpage = take(grow);
     L.query = take(query);
     // From each peer: d / S elements of its outputs, its G references and sums
-    // (and a factor for each of them).
+    // (and a share for each of them).
     L.inbox = take(S > 1 ? 4 * ((size_t)s.G * D + 3 * (size_t)s.G * S) : 0);
     L.total = at;
     return L;
@@ -383,17 +382,17 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 4 ? 4 : 2) paged_decode
         held.attend(run, q, G, g.s.scale * kLog2e);
     }
 
-    // Merge: the CTA's warps, then the cluster's CTAs.  f: a warp's factor for
-    // the CTA's reference, then a CTA's for the last one.
+    // Merge: the CTA's warps, then the cluster's CTAs, by their shares of the
+    // normalising sum.
     __syncthreads();                                 // the rings are done with
     float* om = reinterpret_cast<float*>(sm + L.merge);          // [kWarps][G][D]
     float* rm = om + kWarps * G * D;                             // [kWarps][G] references
     float* lm = rm + kWarps * G;                                 // [kWarps][G] sums
-    float* fm = lm + kWarps * G;                                 // [kWarps][G] factors
+    float* fm = lm + kWarps * G;                                 // [kWarps][G] shares
     run.store(om + warp * G * D, rm + warp * G, lm + warp * G, G, lane);
     __syncthreads();
     const int part = D / S, lg = __ffs(part) - 1;    // elements of a head's output that a CTA combines
-    float* inbox = reinterpret_cast<float*>(sm + L.inbox);       // [S][G][part], then [S][G] references, sums, factors
+    float* inbox = reinterpret_cast<float*>(sm + L.inbox);       // [S][G][part], then [S][G] references, sums, shares
     float* ibr = inbox + G * D;
     float* ibl = ibr + S * G;
     float* ibf = ibl + S * G;
@@ -403,8 +402,8 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 4 ? 4 : 2) paged_decode
         const int hd = tid / 8, w = tid % 8;
         const bool is = hd < G && w < kWarps;
         float M = is ? rm[w * G + hd] : kFloor, l = is ? lm[w * G + hd] : 0.f;
-        const float f = join_parts<8>(M, l);
-        if (is) fm[w * G + hd] = S > 1 ? f : f / l;
+        const float f = join_parts<8>(M, l, S == 1);
+        if (is) fm[w * G + hd] = f;
         if (S > 1) {
             if (hd < G && w < S) {
                 sm100::st_cluster_f32(peer_addr(smem_u32(ibr + rank * G + hd), w), M);
@@ -432,8 +431,8 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 4 ? 4 : 2) paged_decode
         const int hd = tid / 8, c = tid % 8;
         const bool is = hd < G && c < S;
         float M = is ? ibr[c * G + hd] : kFloor, l = is ? ibl[c * G + hd] : 0.f;
-        const float f = join_parts<8>(M, l);
-        if (is) ibf[c * G + hd] = f / l;
+        const float f = join_parts<8>(M, l, true);
+        if (is) ibf[c * G + hd] = f;
         if (is && c == 0 && rank == 0) g.lse[head0 + hd] = (M + log2f(l)) * kLn2;
     }
     __syncthreads();

@@ -7,7 +7,7 @@
 // of all units (batch, kv-head) stand in one row, each unit's led by kOpen that
 // stand for its open rows (and for what a unit costs whatever its length), and
 // every CTA takes the same number of neighbours.  A unit that one CTA holds from end to end is finished there;
-// the parts of the others (output, reference and sum of each head) go to the
+// the parts of the others (mean, reference and sum of each head) go to the
 // workspace, and a second kernel joins them.  Which CTA has what follows from
 // the positions, which both kernels read on the device.
 //
@@ -199,10 +199,10 @@ __global__ void __launch_bounds__(kThreads, kPerSm) paged_dense_kernel(const __g
         }
         held.attend(run, q, G, g.s.scale * kLog2e);
 
-        // The warps' parts meet; f: a warp's factor.
+        // The warps' parts meet; f: a warp's share of the sum.
         __syncthreads();
         float* om = reinterpret_cast<float*>(sm);    // [kWarps][G][D]
-        float* rm = om + kWarps * G * D;             // [kWarps][G] references, then sums, then factors
+        float* rm = om + kWarps * G * D;             // [kWarps][G] references, then sums, then shares
         float* lm = rm + kWarps * G;
         float* fm = lm + kWarps * G;
         run.store(om + warp * G * D, rm + warp * G, lm + warp * G, G, lane);
@@ -213,8 +213,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) paged_dense_kernel(const __g
             const int hd = tid / 8, w = tid % 8;
             const bool is = hd < G && w < kWarps;
             float M = is ? rm[w * G + hd] : kFloor, l = is ? lm[w * G + hd] : 0.f;
-            const float f = join_parts<8>(M, l);
-            if (is) fm[w * G + hd] = whole ? f / l : f;
+            const float f = join_parts<8>(M, l, whole);
+            if (is) fm[w * G + hd] = f;
             if (is && w == 0) {
                 if (whole) {
                     g.lse[head0 + hd] = (M + log2f(l)) * kLn2;
@@ -295,22 +295,23 @@ template <int D, int kJoinThreads> __global__ void __launch_bounds__(kJoinThread
         top = M;
 #pragma unroll
         for (int w = 0; w < kParts / 32; ++w) top = fmaxf(top, s_red[0][w]);
-        const float back = ex2(M - top), f = ex2(r - top);
+        const float before = l * ex2(M - top);
         M = top;
-        if (tid < m) s_f[tid] = f;
-        float sum = s * f;
+        float sum = s * ex2(r - top);
+        if (tid < m) s_f[tid] = sum;
 #pragma unroll
         for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
         if (lane == 0) s_red[1][tid / 32] = sum;
         __syncthreads();
-        l *= back;
+        l = before;
 #pragma unroll
         for (int w = 0; w < kParts / 32; ++w) l += s_red[1][w];
+        const float inv = l == 0.f ? 0.f : 1.f / l, back = before * inv;
         o.x *= back; o.y *= back; o.z *= back; o.w *= back;
 #pragma unroll 8
         for (int c = lot; c < m; c += kLots) {
             const float4 v = reinterpret_cast<const float4*>(part_of(p0 + c) + hd * D)[e];
-            const float x = s_f[c];
+            const float x = s_f[c] * inv;
             o.x = fmaf(v.x, x, o.x);
             o.y = fmaf(v.y, x, o.y);
             o.z = fmaf(v.z, x, o.z);
@@ -324,7 +325,7 @@ template <int D, int kJoinThreads> __global__ void __launch_bounds__(kJoinThread
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < kLots; ++i) sum += reinterpret_cast<const float*>(s_o[i])[tid];
-    g.O[out * D + tid] = sum / l;
+    g.O[out * D + tid] = l == 0.f ? NAN : sum;       // (all scores below float32)
     if (tid == 0) g.lse[out] = (M + log2f(l)) * kLn2;
 }
 
