@@ -58,7 +58,9 @@ namespace hga {
 namespace paged {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kFloor = -1e30f;                     // R of a warp that has met no key
+// R of a warp that has met no key, and a score like any other: the lowest of
+// float32, so that no key is missed for being far below zero.
+constexpr float kFloor = -3.402823466e38f;
 constexpr float kBelow = 12.f, kAbove = 32768.f;      // of W in log2; of a weight
 constexpr int kLeastV = -90;                         // log2 of the smallest values that W follows
 // Keys further below R than this count as if they were there, so that v 2^-W

@@ -103,3 +103,20 @@ def test_scores_past_the_integers_of_float32(values, power, dtype, kind, d):
     for rows in (False, True):
         O, lse, _, _ = _decode(c, [599], q, rows=rows)
         _one_takes_all(c, kind, 0, q, O[0], lse[0], 599)
+
+
+@pytest.mark.parametrize("dtype,kind,d", KINDS)
+@pytest.mark.parametrize("power", [95, 104, 114])
+@pytest.mark.parametrize("n", [1, 40, 300])
+def test_every_score_far_below_zero(n, power, dtype, kind, d):
+    # All keys against the query: the highest score is still below -2^95.
+    p = _params(1, 4, 1, d, 8, 5, dtype, kind)
+    c, q = _filled(p, kind, [n], seed=3)
+    q = (q.float().abs() * 2.0 ** power).to(q.dtype)
+    codes = c.k_pages.view(torch.uint8)
+    codes.copy_(torch.where(codes < 128, 256 - codes.int(), codes.int()).byte() if kind == "int8" else codes | 128)
+    c.k_tail.copy_(-c.k_tail.abs())
+    for rows in (False, True):
+        O, lse, _, _ = _decode(c, [n - 1], q, rows=rows)
+        assert (lse < -2.0 ** power).all()
+        _one_takes_all(c, kind, 0, q, O[0], lse[0], n - 1)
