@@ -27,7 +27,8 @@
 // Precision.  Codes are exact in float16 (int8: at most 127; e4m3: 4
 // significant bits).  A bf16 query is exact in float16 too once its row is
 // scaled by a power of two (elements 2^-27 below the row's largest lose
-// bits: their products are below the sum's rounding); a float32 query, and
+// bits: their products are below the sum's rounding; so do rows below
+// 2^-120, where the scaling ends); a float32 query, and
 // every weight, is the sum of two float16 parts, which carry 2^-24 of it.
 // Sums are float32.
 //
@@ -339,10 +340,11 @@ template <typename TIn, int D> struct Query {
             }
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-        // 2^(13 - floor(log2 top)), by the exponent's bits; 1 for rows of zeros
-        // and of infinities.
+        // 2^(13 - floor(log2 top)), by the exponent's bits, at most 2^120 (its
+        // inverse times `scale` is to stay a normal float32); 1 for rows of
+        // zeros and of infinities.
         const int ex = int(__float_as_uint(top) >> 23);
-        const int sh = ex == 0 || ex == 255 ? 0 : min(max(13 - (ex - 127), -126), 100);
+        const int sh = ex == 0 || ex == 255 ? 0 : min(max(13 - (ex - 127), -126), 120);
         const float up = __uint_as_float(uint32_t(127 + sh) << 23), down = __uint_as_float(uint32_t(127 - sh) << 23);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)

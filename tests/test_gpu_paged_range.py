@@ -120,3 +120,15 @@ def test_every_score_far_below_zero(n, power, dtype, kind, d):
         O, lse, _, _ = _decode(c, [n - 1], q, rows=rows)
         assert (lse < -2.0 ** power).all()
         _one_takes_all(c, kind, 0, q, O[0], lse[0], n - 1)
+
+
+@pytest.mark.parametrize("dtype,kind,d", KINDS)
+@pytest.mark.parametrize("power", [60, 100, 112, 118])
+def test_small_queries_of_large_keys(power, dtype, kind, d):
+    # Scores of ordinary size from queries of 2^-118 and keys of 2^118.
+    p = _params(2, 8, 2, d, 24, 11, dtype, kind, 3, 13)
+    c, q = _filled(p, kind, [640, 300], seed=5)
+    q = (q.float() * 2.0 ** -power).to(q.dtype)
+    for t in (c.k_scale, c.k_tail, c.csum, c.gsum):
+        t *= 2.0 ** power
+    _both(p, kind, c, [639, 299], q)
