@@ -258,25 +258,25 @@ __device__ __forceinline__ void append_chunk(const Args& g, const Seq& q, int b,
     const int64_t rows = (ph * kChunk + warp * kGroup) * D;
     close_group<CACHE, D, R>(k, static_cast<uint8_t*>(g.c.k_pages) + rows, g.c.k_scale + ph * kGroupsPerChunk + warp, un,
                              rl, RL, lane);
-    // Summaries: the group's sum over its 8 rows, then the chunk's over 8 groups.
-    float sum[16];
+    // Summaries: the group's mean over its 8 rows, then the chunk's over 8 groups.
+    // Each term is divided (by a power of two) before it is added: a mean of
+    // finite keys is finite where their sum is not.
+    float mean[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-        float t = k[0][e];
+        float t = k[0][e] * (1.0f / kGroup);
 #pragma unroll
-        for (int j = 1; j < R; ++j) t += k[j][e];
+        for (int j = 1; j < R; ++j) t = fmaf(k[j][e], 1.0f / kGroup, t);
 #pragma unroll
         for (int o = U; o < 32; o <<= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-        sum[e] = t;
+        mean[e] = t;
     }
     if (rl == 0) {
-        store8(&part[warp][un.a], sum);
-        store8(&part[warp][un.b], sum + 8);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) sum[e] *= 1.0f / kGroup;
+        store8(&part[warp][un.a], mean);
+        store8(&part[warp][un.b], mean + 8);
         float* dst = g.c.gsum + (ph * kGroupsPerChunk + warp) * D;
-        store8(dst + un.a, sum);
-        store8(dst + un.b, sum + 8);
+        store8(dst + un.a, mean);
+        store8(dst + un.b, mean + 8);
     }
 #pragma unroll
     for (int j = 0; j < R; ++j) {
@@ -289,8 +289,8 @@ __device__ __forceinline__ void append_chunk(const Args& g, const Seq& q, int b,
     for (int e = tid; e < D; e += kThreads) {
         float t = 0.f;
 #pragma unroll
-        for (int w = 0; w < kGroupsPerChunk; ++w) t += part[w][e];
-        g.c.csum[ph * D + e] = t * (1.0f / kChunk);
+        for (int w = 0; w < kGroupsPerChunk; ++w) t = fmaf(part[w][e], 1.0f / kGroupsPerChunk, t);
+        g.c.csum[ph * D + e] = t;
     }
 }
 

@@ -16,7 +16,7 @@ import torch
 import hierarchical_routed_sparse_b200 as hga
 
 import paged_ref as R
-from test_gpu_paged import TENSORS, _cache, _check_decode, _decode, _filled, _int32, _params
+from test_gpu_paged import TENSORS, Plain, _cache, _check_decode, _decode, _filled, _int32, _params, _snapshot
 
 pytestmark = pytest.mark.gpu
 KINDS = [("bf16", "int8", 128), ("fp32", "e4m3", 64), ("fp32", "int8", 64), ("bf16", "e4m3", 128)]
@@ -132,3 +132,27 @@ def test_small_queries_of_large_keys(power, dtype, kind, d):
     for t in (c.k_scale, c.k_tail, c.csum, c.gsum):
         t *= 2.0 ** power
     _both(p, kind, c, [639, 299], q)
+
+
+@pytest.mark.parametrize("dtype,kind,d", KINDS)
+@pytest.mark.parametrize("power", [0, 121, 124, 126])
+def test_summaries_of_the_largest_keys(power, dtype, kind, d):
+    # Keys of one sign whose sums over a group (from 2^125 on) or a chunk (from
+    # 2^122) are past float32, while their means are not; codes, scales and open
+    # rows as everywhere.
+    p = _params(1, 4, 2, d, 4, 3, dtype, kind, 1, 5)
+    c = _cache(p)
+    plain, before = Plain(p, kind, c.table), _snapshot(c)
+    g = torch.Generator().manual_seed(power)
+    k = ((1 + torch.rand(130, 2, d, generator=g)) * 2.0 ** power).to(p.torch_dtype).cuda()
+    v = torch.randn(130, 2, d, generator=g).to(p.torch_dtype).cuda()
+    at = 0
+    for n in (60, 66, 4):
+        c.append(_int32([at]), k[at:at + n], v[at:at + n], cu=_int32([0, n]))
+        at += n
+    torch.cuda.synchronize()
+    plain.append(0, k, v, None, False)
+    plain.check(c, before)
+    q = (torch.randn(1, 4, d, generator=g) * 2.0 ** -min(power, 118)).to(p.torch_dtype).cuda()
+    _both(p, kind, c, [129], q)
+    assert hga.device_check() == 0
