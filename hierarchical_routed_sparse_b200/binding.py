@@ -31,7 +31,7 @@ EXPORTS = ("hga_route_widths", "hga_workspace_size", "hga_build_summaries", "hga
            "hga_stage_params", "hga_stage_routed", "hga_decode", "hga_route_causal", "hga_causal_sched_size",
            "hga_causal_schedule", "hga_attn_fwd_causal", "hga_attn_bwd_causal", "hga_device_status", "hga_device_check", "hga_checked_build",
            "hga_rope_fwd", "hga_rope_bwd", "hga_paged_widths", "hga_paged_workspace_size", "hga_paged_append",
-           "hga_paged_decode", "hga_selftest_wait", "hga_last_error",
+           "hga_paged_advance", "hga_paged_decode", "hga_selftest_wait", "hga_last_error",
            "hga_version")
 NOALLOC_MAX_ROWS = 1 << 20     # HGA_NOALLOC_MAX_ROWS
 
@@ -156,6 +156,7 @@ def load() -> ctypes.CDLL:
             "hga_paged_workspace_size": ([ctypes.POINTER(_PagedParams)], ctypes.c_size_t),
             "hga_paged_append": ([ctypes.POINTER(_PagedParams), ctypes.POINTER(_PagedCache), P, P, I64, P, I64, I64,
                                   P, I64, I64, P, I64, I64, P, P, I64, ctypes.c_int, ctypes.c_int, P], ctypes.c_int),
+            "hga_paged_advance": ([ctypes.POINTER(_PagedParams), P, P, I64, I64, ctypes.c_int, P, P], ctypes.c_int),
             "hga_paged_decode": ([ctypes.POINTER(_PagedParams), ctypes.POINTER(_PagedCache), P, P, P, P, P, P, P,
                                   ctypes.c_size_t, P], ctypes.c_int),
             "hga_device_status": ([ctypes.POINTER(ctypes.c_int), ctypes.c_int], ctypes.c_int),

@@ -661,6 +661,18 @@ size_t hga_paged_workspace_size(const hga_paged_params* p)
     return s.k_c > 0 || s.k_g > 0 ? 0 : hga::paged_dense_workspace(s);
 }
 
+// Token count and rotation extent of an append call.
+static int check_tokens(const hga::PagedShape& s, const int32_t* cu_tokens, int64_t N, int rot_dim, int64_t rope_rows)
+{
+    if (N < 0 || N > INT32_MAX) return fail(HGA_ERR_INVALID_ARG, "N (%lld) must lie in [0, 2^31)", (long long)N);
+    if (!cu_tokens && N != s.B)
+        return fail(HGA_ERR_INVALID_ARG, "without cu_tokens N (%lld) must be B (%d): one token each", (long long)N, s.B);
+    if (rot_dim < 0 || rot_dim > s.d || rot_dim % 16)
+        return fail(HGA_ERR_INVALID_ARG, "rot_dim (%d) must be a multiple of 16 in [0, d=%d]", rot_dim, s.d);
+    if (rot_dim > 0 && rope_rows < 1) return fail(HGA_ERR_INVALID_ARG, "rope_rows (%lld) must be >= 1", (long long)rope_rows);
+    return HGA_OK;
+}
+
 int hga_paged_append(const hga_paged_params* p, const hga_paged_cache* c, const int32_t* pos,
                      const int32_t* cu_tokens, int64_t N, const void* q, int64_t q_token, int64_t q_head,
                      const void* k, int64_t k_token, int64_t k_head, const void* v, int64_t v_token,
@@ -670,11 +682,8 @@ int hga_paged_append(const hga_paged_params* p, const hga_paged_cache* c, const 
     const NvtxRange nvtx_range("hga_paged_append");
     hga::PagedShape s{};
     if (int r = paged_shape(p, &s)) return r;
-    if (N < 0 || N > INT32_MAX) return fail(HGA_ERR_INVALID_ARG, "N (%lld) must lie in [0, 2^31)", (long long)N);
-    if (!cu_tokens && N != s.B)
-        return fail(HGA_ERR_INVALID_ARG, "without cu_tokens N (%lld) must be B (%d): one token each", (long long)N, s.B);
+    if (int r = check_tokens(s, cu_tokens, N, rot_dim, rope_rows)) return r;
     if (int r = check_rotation(rot_dim, s.d, rope, "rope")) return r;
-    if (rot_dim > 0 && rope_rows < 1) return fail(HGA_ERR_INVALID_ARG, "rope_rows (%lld) must be >= 1", (long long)rope_rows);
     const int el = element_bytes(s.dtype);
     if (int r = check_stride(k_token, el, "k_token")) return r;
     if (int r = check_stride(k_head, el, "k_head")) return r;
@@ -699,6 +708,25 @@ int hga_paged_append(const hga_paged_params* p, const hga_paged_cache* c, const 
     if (!hga::paged_append_grid_fits(s, a)) return fail(HGA_ERR_UNSUPPORTED, "problem too large for one launch grid");
     const auto st = static_cast<cudaStream_t>(stream);
     return finish(hga::launch_paged_append(s, *c, a, st), st, "hga_paged_append");
+}
+
+int hga_paged_advance(const hga_paged_params* p, int32_t* pos, const int32_t* cu_tokens, int64_t N, int64_t rope_rows,
+                      int rot_dim, int32_t* last, hga_stream_t stream)
+{
+    const NvtxRange nvtx_range("hga_paged_advance");
+    hga::PagedShape s{};
+    if (int r = paged_shape(p, &s)) return r;
+    if (int r = check_tokens(s, cu_tokens, N, rot_dim, rope_rows)) return r;
+    if (!pos) return fail(HGA_ERR_INVALID_ARG, "pos is NULL");
+    if (pos == last) return fail(HGA_ERR_INVALID_ARG, "pos and last are the same");
+    hga::PagedAppend a{};
+    a.pos = pos;
+    a.cu = cu_tokens;
+    a.N = N;
+    a.rot = rot_dim;
+    a.rope_rows = rope_rows;
+    const auto st = static_cast<cudaStream_t>(stream);
+    return finish(hga::launch_paged_advance(s, a, pos, last, st), st, "hga_paged_advance");
 }
 
 int hga_paged_decode(const hga_paged_params* p, const hga_paged_cache* c, const int32_t* pos, const void* q,

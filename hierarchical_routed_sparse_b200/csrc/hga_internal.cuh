@@ -231,6 +231,7 @@ bool rope_grid_fits(const RopeShape& s);
 // paged_dense.cu).
 cudaError_t launch_paged_append(const PagedShape& s, const hga_paged_cache& c, const PagedAppend& a, cudaStream_t st);
 bool paged_append_grid_fits(const PagedShape& s, const PagedAppend& a);
+cudaError_t launch_paged_advance(const PagedShape& s, const PagedAppend& a, int32_t* pos, int32_t* last, cudaStream_t st);
 cudaError_t launch_paged_routed(const PagedShape& s, const hga_paged_cache& c, const int32_t* pos, const void* q,
                                 float* O, float* lse, int32_t* cidx, int32_t* gidx, cudaStream_t st);
 size_t paged_routed_smem(const PagedShape& s);

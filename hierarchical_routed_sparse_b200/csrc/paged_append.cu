@@ -21,6 +21,10 @@
 // and three dependent loads for single tokens (2 us for one sequence, 7 us
 // for 64 of which eight complete a chunk).
 //
+// Positions are moved by a call of their own, behind the rule that the append
+// itself goes by (sequence()): by what it took, so that an empty slot stays
+// empty and a position never counts a token that is not in the cache.
+//
 // Rows of the open chunk that were there before are read when the chunk
 // closes.  Where the same call also fills a later chunk, whose rows take
 // their place, one CTA does both, in this order.
@@ -386,6 +390,19 @@ __global__ void __launch_bounds__(kThreads, sizeof(TIn) * D < 512 ? 3 : 2) paged
     }
 }
 
+// pos[b] moves by the tokens that an append of the same arguments takes; last[b]
+// (where wanted) is the position of the last of them, or -1.
+__global__ void __launch_bounds__(kThreads) paged_advance_kernel(const __grid_constant__ Args g, int32_t* pos, int32_t* last)
+{
+    pdl_wait();
+    pdl_trigger();
+    const int64_t b = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (b >= g.s.B) return;
+    const Seq q = sequence(g, (int)b);
+    if (q.n > 0) pos[b] = q.pos + q.n;
+    if (last) last[b] = q.n > 0 ? q.pos + q.n - 1 : -1;
+}
+
 int64_t items_of(const PagedShape& s, const PagedAppend& a)
 {
     // A sequence's n tokens touch at most n / 64 + 2 chunks, and at most n.
@@ -425,6 +442,13 @@ cudaError_t launch_paged_append(const PagedShape& s, const hga_paged_cache& c, c
     if (s.dtype == HGA_BF16)
         return s.d == 128 ? by_cache<__nv_bfloat16, 128>(g, items, st) : by_cache<__nv_bfloat16, 64>(g, items, st);
     return s.d == 128 ? by_cache<float, 128>(g, items, st) : by_cache<float, 64>(g, items, st);
+}
+
+cudaError_t launch_paged_advance(const PagedShape& s, const PagedAppend& a, int32_t* pos, int32_t* last, cudaStream_t st)
+{
+    const Args g{s, {}, a, 0, false};
+    return launch_pdl(paged_advance_kernel, dim3((unsigned)(((int64_t)s.B + kThreads - 1) / kThreads)), dim3(kThreads), 0, st, g,
+                      pos, last);
 }
 
 HGA_CHECK_WORD_READER(check_word_paged_append)

@@ -2,7 +2,7 @@
 
 ``PagedCache`` holds the cache's tensors and calls the library on them:
 ``append`` puts tokens into it (rotating queries and keys on the way),
-``decode`` lets one query per sequence attend it.  Which page a chunk gets is
+``advance`` moves the positions by what it took, ``decode`` lets one query per sequence attend it.  Which page a chunk gets is
 the caller's choice, written into ``table``; ``PagedDecodeState`` hands pages
 out in order and generates token by token, as ``DecodeState`` does on a dense
 cache.  Positions and tables live on the device, so a captured step serves
@@ -101,7 +101,7 @@ class PagedCache:
         n = paged_workspace_size(p)
         self.workspace = torch.empty(n, dtype=torch.uint8, device=self.table.device) if n else None
         lib = B.load()
-        self._append, self._decode = lib.hga_paged_append, lib.hga_paged_decode
+        self._append, self._advance, self._decode = lib.hga_paged_append, lib.hga_paged_advance, lib.hga_paged_decode
         self._dtype = p.torch_dtype
 
     def _rows(self, t, name, N, H, dev):
@@ -134,6 +134,25 @@ class PagedCache:
         if code:
             B._check(code)
 
+    def advance(self, pos, cu=None, N=None, rope=None, last=None, stream=None):
+        """pos[b] (int32, device) grows by the tokens that ``append`` took for
+        sequence b from the same pos, cu and rope, N tokens in all (B without
+        cu); none for an empty slot or past the cache's or the rotation
+        table's end.  last [B] (int32) gets the position of the last one, or
+        -1 where there was none."""
+        p, dev = self.p, torch.cuda.current_device()
+        if N is None:
+            if cu is not None:
+                raise ValueError("advance with offsets needs N, the tokens of the append")
+            N = p.B
+        rows, rot = (0, 0) if rope is None else rope.shape
+        code = self._advance(
+            self._pp, _dense(pos, "pos", (p.B,), torch.int32, dev),
+            None if cu is None else _dense(cu, "cu", (p.B + 1,), torch.int32, dev), N, rows, rot,
+            None if last is None else _dense(last, "last", (p.B,), torch.int32, dev), B._raw_stream(stream, dev))
+        if code:
+            B._check(code)
+
     def decode(self, pos, q, O, lse, cidx=None, gidx=None, workspace=None, stream=None):
         """The query q [B][Hq][d] of each sequence, at position pos[b] (int32,
         device; negative: empty), attends its cache: O [B][Hq][d] and lse
@@ -163,7 +182,10 @@ class PagedDecodeState:
     b * max_chunks + c.  ``prefill`` appends prompts, each ``step`` appends one
     token per sequence and attends; both rotate by ``rope`` (``rope_table``)
     when it is given.  ``pos`` counts the tokens in the cache; ``step``
-    advances it on the device, so a step can be captured and replayed."""
+    advances it on the device, so a step can be captured and replayed.  A
+    negative ``pos[b]`` is an empty slot: its tokens are passed over, its O is
+    0, and it stays as it is until the program writes another position there
+    (the old one, to go on with a sequence that was held)."""
 
     def __init__(self, B_: int, Hq: int, Hkv: int, d: int, max_tokens: int, k_c: int, k_g: int, dtype: int = HGA_BF16,
                  cache_dtype: int = HGA_INT8, scale: float = 0.0, rope=None, interleaved: bool = False,
@@ -179,7 +201,7 @@ class PagedDecodeState:
         self.O = torch.empty(B_, Hq, d, device=device, dtype=torch.float32)
         self.lse = torch.empty(B_, Hq, device=device, dtype=torch.float32)
         self.q = torch.empty(B_, Hq, d, device=device, dtype=p.torch_dtype)
-        self.pos = torch.zeros(B_, **i32)            # tokens in the cache
+        self.pos = torch.zeros(B_, **i32)            # tokens in the cache; negative: an empty slot
         self.rope, self.interleaved = rope, interleaved
 
     def prefill(self, k, v, cu, stream=None):
@@ -187,7 +209,7 @@ class PagedDecodeState:
         cu[b] .. cu[b + 1] - 1 (int32, device)."""
         with torch.cuda.stream(stream or torch.cuda.current_stream()):
             self.cache.append(self.pos, k, v, cu=cu, rope=self.rope, interleaved=self.interleaved)
-            self.pos += cu[1:] - cu[:-1]
+            self.cache.advance(self.pos, cu=cu, N=k.shape[0], rope=self.rope)
 
     def step(self, q, k, v, stream=None):
         """The next token of every sequence: q [B][Hq][d], k, v [B][Hkv][d];
@@ -195,5 +217,5 @@ class PagedDecodeState:
         with torch.cuda.stream(stream or torch.cuda.current_stream()):
             self.cache.append(self.pos, k, v, q=q, q_out=self.q, rope=self.rope, interleaved=self.interleaved)
             self.cache.decode(self.pos, self.q, self.O, self.lse, self.cidx, self.gidx)
-            self.pos += 1
+            self.cache.advance(self.pos, rope=self.rope)
         return self.O

@@ -430,6 +430,16 @@ int hga_paged_append(const hga_paged_params* p, const hga_paged_cache* c, const 
                      int64_t v_head, void* q_out, const float* rope, int64_t rope_rows, int rot_dim,
                      int interleaved, hga_stream_t stream);
 
+/* Positions after an append: pos[b] grows by the number of tokens that
+ * hga_paged_append takes for sequence b when it is called with the same pos,
+ * cu_tokens, N, rope_rows and rot_dim: none for an empty slot, which stays as
+ * it is, and none past the table's width or the rotation table's rows
+ * (recorded, as there).  last [B], unless NULL, gets the position of the last
+ * token taken, or -1 where none was: what hga_paged_decode is given when the
+ * append was a generation step.  pos and last must not overlap. */
+int hga_paged_advance(const hga_paged_params* p, int32_t* pos, const int32_t* cu_tokens, int64_t N,
+                      int64_t rope_rows, int rot_dim, int32_t* last, hga_stream_t stream);
+
 /* Row widths of the index tables: wc = k_c (max_chunks for HGA_ALL); wg = k_g
  * (8 * wc for HGA_ALL). */
 int hga_paged_widths(const hga_paged_params* p, int* wc, int* wg);
@@ -480,8 +490,8 @@ int hga_device_status(int* status, int clear);
  * In that build hga_route_groups, hga_attn_fwd, hga_attn_bwd,
  * hga_attn_bwd_noalloc, hga_stage_routed, hga_attn_fwd_causal and
  * hga_attn_bwd_causal wait for their stream and return HGA_ERR_DEVICE_CHECK
- * (outputs invalid, word cleared) when a check failed; hga_paged_append and
- * hga_paged_decode, which check their device data in every build, report it
+ * (outputs invalid, word cleared) when a check failed; hga_paged_append,
+ * hga_paged_advance and hga_paged_decode, which check their device data in every build, report it
  * so as well.  Release builds skip the other checks and return without
  * waiting.
  * hga_checked_build: 1 in a checked build, else 0.

@@ -190,3 +190,15 @@ def test_plain_quantisation_is_within_half_a_step(cache):
     step = 0.5 * (1 + 2e-4) if cache == "int8" else 2.0 ** -10
     tol = step * scale[:, None, None].astype(np.float64) + (0 if cache == "int8" else 2.0 ** -4 * (1 + 2e-6) * np.abs(x))
     assert (err <= tol).all()
+
+
+def test_advance_refusals(lib):
+    def call(p=None, pos=P16, cu=P16, N=5, rows=100, rot=128, last=ctypes.c_void_p(32)):
+        return lib.hga_paged_advance(ctypes.byref((p or _paged()).c()), pos, cu, N, rows, rot, last, None)
+
+    for kw, code in ((dict(pos=None), BAD), (dict(N=-1), BAD), (dict(N=1 << 31), BAD), (dict(cu=None), BAD), (dict(rot=24), BAD),
+                     (dict(rot=144), BAD), (dict(rows=0), BAD), (dict(last=P16), BAD), (dict(p=_paged(d=96)), UNSUP),
+                     (dict(p=_paged(B=0)), BAD)):
+        assert call(**kw) == code, kw
+        assert lib.hga_last_error().decode()
+    assert lib.hga_paged_advance(None, P16, None, 2, 1, 0, None, None) == BAD
