@@ -185,12 +185,26 @@ class PagedDecodeState:
     advances it on the device, so a step can be captured and replayed.  A
     negative ``pos[b]`` is an empty slot: its tokens are passed over, its O is
     0, and it stays as it is until the program writes another position there
-    (the old one, to go on with a sequence that was held)."""
+    (the old one, to go on with a sequence that was held).
+
+    ``capacity`` is the most that a sequence can hold: the pages (``max_tokens``
+    rounded up to whole chunks) or the rotation table's rows, which must not be
+    fewer than ``max_tokens``.  What goes past it is not taken: ``pos`` stays,
+    O is 0, and the fault is recorded on the device (``device_check``), since
+    only the device knows the positions."""
 
     def __init__(self, B_: int, Hq: int, Hkv: int, d: int, max_tokens: int, k_c: int, k_g: int, dtype: int = HGA_BF16,
                  cache_dtype: int = HGA_INT8, scale: float = 0.0, rope=None, interleaved: bool = False,
                  device="cuda"):
+        if max_tokens < 1:
+            raise ValueError(f"max_tokens must be >= 1 (got {max_tokens})")
         chunks = -(-max_tokens // 64)
+        self.capacity = 64 * chunks
+        if rope is not None:
+            B._check_table(rope, "rope")
+            if rope.shape[0] < max_tokens:
+                raise ValueError(f"a rotation table of {rope.shape[0]} rows is shorter than max_tokens={max_tokens}")
+            self.capacity = min(self.capacity, rope.shape[0])
         self.p = p = PagedParams(B_, Hq, Hkv, d, B_ * chunks, chunks, k_c, k_g, dtype, cache_dtype, scale)
         i32 = dict(device=device, dtype=torch.int32)
         self.cache = PagedCache(p, table=torch.arange(B_ * chunks, **i32).view(B_, chunks))
@@ -202,6 +216,7 @@ class PagedDecodeState:
         self.lse = torch.empty(B_, Hq, device=device, dtype=torch.float32)
         self.q = torch.empty(B_, Hq, d, device=device, dtype=p.torch_dtype)
         self.pos = torch.zeros(B_, **i32)            # tokens in the cache; negative: an empty slot
+        self.last = torch.full((B_,), -1, **i32)     # position of each sequence's newest token in a step, -1: it got none
         self.rope, self.interleaved = rope, interleaved
 
     def prefill(self, k, v, cu, stream=None):
@@ -216,6 +231,6 @@ class PagedDecodeState:
         returns O [B][Hq][d] (float32, the state's buffer)."""
         with torch.cuda.stream(stream or torch.cuda.current_stream()):
             self.cache.append(self.pos, k, v, q=q, q_out=self.q, rope=self.rope, interleaved=self.interleaved)
-            self.cache.decode(self.pos, self.q, self.O, self.lse, self.cidx, self.gidx)
-            self.cache.advance(self.pos, rope=self.rope)
+            self.cache.advance(self.pos, rope=self.rope, last=self.last)
+            self.cache.decode(self.last, self.q, self.O, self.lse, self.cidx, self.gidx)
         return self.O

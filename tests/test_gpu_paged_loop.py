@@ -173,3 +173,35 @@ def test_a_full_sequence_does_not_count_on(dtype, kind, k_c, k_g):
     st.prefill(k, v, _int32([0, 0, 130]))
     assert st.pos.tolist() == [128, 128]
     assert hga.device_check(clear=True) == 413
+
+
+@pytest.mark.parametrize("dtype,kind,k_c,k_g", FORMS)
+@pytest.mark.parametrize("rows", [100, 127])
+def test_a_rotation_table_that_ends_inside_the_last_chunk(rows, dtype, kind, k_c, k_g):
+    # The table ends before the pages do: past its last row a token is not taken
+    # and nothing is answered from what is left of the step before.
+    rope = hga.rope_table(rows, 64)
+    st = _state(2, 100, dtype, kind, k_c, k_g, rope)
+    assert st.capacity == rows
+    plain = Plain(st.p, kind, st.cache.table)
+    _, k, v = _tokens(st.p, rows + 2, 9)
+    st.prefill(k, v, _int32([0, rows - 2, rows + 2]))
+    for b, s in ((0, slice(0, rows - 2)), (1, slice(rows - 2, rows + 2))):
+        plain.append(b, k[s], v[s], rope, False)
+    assert hga.device_check(clear=True) == 0
+    for i, seed in enumerate(_captured(st, range(6))):
+        _check_step(st, kind, plain, rope, seed, (0, 1) if i < 2 else (1,))
+        assert st.pos.tolist() == [min(rows - 1 + i, rows), 5 + i]
+        assert hga.device_check(clear=True) == (413 if i >= 2 else 0)
+
+
+def test_limits_that_the_host_knows():
+    with pytest.raises(ValueError, match="shorter"):
+        _state(1, 129, "bf16", "int8", 2, 9, hga.rope_table(128, 64))
+    st = _state(2, 100, "bf16", "int8", 2, 9, None)
+    assert st.capacity == 128
+    _, k, v = _tokens(st.p, 300, 1)                             # behind the offsets: tokens of no sequence
+    st.prefill(k, v, _int32([0, 100, 120]))
+    assert st.pos.tolist() == [100, 20] and hga.device_check() == 0
+    with pytest.raises(ValueError):
+        _state(1, 0, "bf16", "int8", 2, 9, None)

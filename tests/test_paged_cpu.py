@@ -202,3 +202,9 @@ def test_advance_refusals(lib):
         assert call(**kw) == code, kw
         assert lib.hga_last_error().decode()
     assert lib.hga_paged_advance(None, P16, None, 2, 1, 0, None, None) == BAD
+
+
+def test_a_generation_state_needs_a_long_enough_table(lib):
+    for tokens, rope in ((129, torch.zeros(128, 64)), (0, None), (64, torch.zeros(64, 64).double())):
+        with pytest.raises(ValueError, match="rope|rotation|max_tokens"):       # before any device tensor is made
+            hga.PagedDecodeState(1, 4, 2, 64, tokens, 2, 9, rope=rope)
