@@ -162,6 +162,8 @@ class PagedCache:
         p, dev = self.p, torch.cuda.current_device()
         wc, wg = self._widths
         ws = self.workspace if workspace is None else workspace
+        if ws is not None and not ws.is_contiguous():          # (its bytes would not be its own)
+            raise ValueError("workspace must be a contiguous tensor")
         code = self._decode(
             self._pp, self._pc, _dense(pos, "pos", (p.B,), torch.int32, dev),
             _dense(q, "q", (p.B, p.Hq, p.d), self._dtype, dev),

@@ -156,3 +156,19 @@ def test_summaries_of_the_largest_keys(power, dtype, kind, d):
     q = (torch.randn(1, 4, d, generator=g) * 2.0 ** -min(power, 118)).to(p.torch_dtype).cuda()
     _both(p, kind, c, [129], q)
     assert hga.device_check() == 0
+
+
+def test_a_workspace_that_is_not_contiguous_is_refused():
+    # As many bytes by its shape as are needed, and far fewer behind its pointer.
+    p = _params(1, 4, 2, 64, 4, 3, "bf16", "int8")
+    c, q = _filled(p, "int8", [100])
+    n = hga.paged_workspace_size(p)
+    O, lse = torch.full((1, 4, 64), 9.0, device="cuda"), torch.full((1, 4), 9.0, device="cuda")
+    for ws in (torch.empty(16, dtype=torch.uint8, device="cuda")[:1].expand(n),
+               torch.empty(2 * n, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError, match="contiguous"):
+            c.decode(_int32([99]), q, O, lse, workspace=ws)
+    torch.cuda.synchronize()
+    assert (O == 9.0).all()
+    c.decode(_int32([99]), q, O, lse, workspace=torch.empty(n // 4, dtype=torch.float32, device="cuda"))
+    _check_decode(c, "int8", [99], q, (O.cpu().numpy(), lse.cpu().numpy(), None, None), rows=False)
