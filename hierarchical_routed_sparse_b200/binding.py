@@ -428,8 +428,8 @@ def _rope(call, src, dst, x, y, table, pos0: int, interleaved: bool, stream) -> 
 
 
 def rope_fwd(x, y, table, pos0: int = 0, interleaved: bool = False, stream=None) -> None:
-    """y [B][H][T][d] = x [B][T][H][d] (any strides with unit stride along d)
-    rotated by positions pos0 + t; ``table`` as of ``rope_table`` (None: no
+    """y [B][H][T][d] = x [B][T][H][d] (by strides of whole 16 bytes, with unit
+    stride along d) rotated by positions pos0 + t; ``table`` as of ``rope_table`` (None: no
     rotation, only the layout and the type change)."""
     _rope(load().hga_rope_fwd, x, y, x, y, table, pos0, interleaved, stream)
 

@@ -521,9 +521,11 @@ int hga_attn_bwd_causal(const hga_params* p, const void* Q, const void* K, const
 
 // ---- position rotation ----------------------------------------------------------
 
-// Rows of `el`-byte elements by strides: non-negative multiples of 16 bytes.
-static int check_stride(int64_t stride, int el, const char* name)
+// Rows of `el`-byte elements by strides: non-negative multiples of 16 bytes
+// (of a dimension of one: anything, it is not used).
+static int check_stride(int64_t stride, int64_t extent, int el, const char* name)
 {
+    if (extent <= 1) return HGA_OK;
     if (stride < 0 || stride % (16 / el))
         return fail(HGA_ERR_INVALID_ARG, "%s (%lld) must be non-negative and span a multiple of 16 bytes", name,
                     (long long)stride);
@@ -560,9 +562,9 @@ static int run_rope(const hga_rope_params* p, bool back, const void* src, const 
         return fail(HGA_ERR_INVALID_ARG, "positions up to %lld exceed the table of %lld rows",
                     (long long)(p->pos0 + p->T), (long long)p->table_rows);
     const int el = element_bytes(p->x_dtype);
-    if (int r = check_stride(p->x_batch, el, "x_batch")) return r;
-    if (int r = check_stride(p->x_token, el, "x_token")) return r;
-    if (int r = check_stride(p->x_head, el, "x_head")) return r;
+    if (int r = check_stride(p->x_batch, p->B, el, "x_batch")) return r;
+    if (int r = check_stride(p->x_token, p->T, el, "x_token")) return r;
+    if (int r = check_stride(p->x_head, p->H, el, "x_head")) return r;
     // Rows that are written must not share elements (what overlaps beyond these
     // bounds is the caller's to avoid).
     if (back && ((p->B > 1 && p->x_batch < p->d) || (p->T > 1 && p->x_token < p->d) || (p->H > 1 && p->x_head < p->d)))
@@ -685,13 +687,13 @@ int hga_paged_append(const hga_paged_params* p, const hga_paged_cache* c, const 
     if (int r = check_tokens(s, cu_tokens, N, rot_dim, rope_rows)) return r;
     if (int r = check_rotation(rot_dim, s.d, rope, "rope")) return r;
     const int el = element_bytes(s.dtype);
-    if (int r = check_stride(k_token, el, "k_token")) return r;
-    if (int r = check_stride(k_head, el, "k_head")) return r;
-    if (int r = check_stride(v_token, el, "v_token")) return r;
-    if (int r = check_stride(v_head, el, "v_head")) return r;
+    if (int r = check_stride(k_token, N, el, "k_token")) return r;
+    if (int r = check_stride(k_head, s.Hkv, el, "k_head")) return r;
+    if (int r = check_stride(v_token, N, el, "v_token")) return r;
+    if (int r = check_stride(v_head, s.Hkv, el, "v_head")) return r;
     if (q) {
-        if (int r = check_stride(q_token, el, "q_token")) return r;
-        if (int r = check_stride(q_head, el, "q_head")) return r;
+        if (int r = check_stride(q_token, N, el, "q_token")) return r;
+        if (int r = check_stride(q_head, s.Hq, el, "q_head")) return r;
     }
     if (!q != !q_out) return fail(HGA_ERR_INVALID_ARG, "q and q_out go together");
     if (N == 0) return HGA_OK;

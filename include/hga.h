@@ -345,7 +345,8 @@ int hga_attn_bwd_causal(const hga_params* p, const void* Q, const void* K,
  *   (x_dtype, strided): the transposed rotation, dx1 = dy1 c + dy2 s,
  *   dx2 = dy2 c - dy1 s.  dx rows are overwritten, not accumulated.
  * rot_dim is a multiple of 16 and at most d; strides are non-negative and
- * span multiples of 16 bytes (x rows may repeat, stride 0; dx rows may not);
+ * span multiples of 16 bytes (those of a dimension of one are not looked at;
+ * x rows may repeat, stride 0; dx rows may not);
  * pos0 + T must not exceed table_rows; T = 0 is no work.  Input and output
  * must not overlap. */
 typedef struct hga_rope_params {
@@ -412,8 +413,8 @@ typedef struct hga_paged_cache {
  * number of tokens that it holds (negative: an empty slot, skipped), and is
  * not changed.  cu_tokens = NULL: one token each (N = B).  Tokens that belong
  * to no sequence (behind cu_tokens[B]) are left alone, in q_out too.
- *   k, v   rows [N][Hkv][d] (dtype) by element strides (token, head), unit
- *          stride along d; q rows [N][Hq][d] alike, or NULL
+ *   k, v   rows [N][Hkv][d] (dtype) by element strides (token, head) as of
+ *          hga_rope_fwd, unit stride along d; q rows [N][Hq][d] alike, or NULL
  *   q_out  [N][Hq][d] (dtype, dense): the rotated queries; no overlap with
  *          the inputs
  *   rope   [rope_rows][rot_dim] as for hga_rope_fwd; rot_dim = 0: the rows

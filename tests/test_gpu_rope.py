@@ -118,3 +118,28 @@ def test_captured_and_replayed():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(y, want)
+
+
+def test_strides_of_dimensions_of_one_do_not_matter():
+    # What such a stride says is nobody's offset (a view made by permute may have
+    # any): contiguous rows are taken, by the rotation and by the append.
+    g = torch.Generator().manual_seed(11)
+    x = torch.randn(5, 3, 64, 1, generator=g).cuda().permute(3, 0, 1, 2)        # [1][5][3][64], batch stride 1
+    assert x.is_contiguous() and x.stride(0) == 1
+    rope = hga.rope_table(16, 64)
+    want, got = torch.empty(1, 3, 5, 64, device="cuda"), torch.empty(1, 3, 5, 64, device="cuda")
+    hga.rope_fwd(x.clone(memory_format=torch.contiguous_format).view(1, 5, 3, 64).as_strided((1, 5, 3, 64), (960, 192, 64, 1)), want, rope)
+    hga.rope_fwd(x, got, rope)
+    assert torch.equal(got, want)
+    back = torch.empty(960, device="cuda").as_strided((1, 5, 3, 64), (1, 192, 64, 1))
+    hga.rope_bwd(want, back, rope)
+    assert float((back - x).abs().max()) < 1e-5
+    one = torch.randn(64, generator=g).bfloat16().cuda().as_strided((1, 1, 64), (3, 1, 1))
+    p = hga.PagedParams(1, 1, 1, 64, 1, 1)
+    caches = [hga.PagedCache(p) for _ in range(2)]
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for c, k in zip(caches, (one, one.clone().view(64).view(1, 1, 64))):
+        out = torch.empty(1, 1, 64, dtype=torch.bfloat16, device="cuda")
+        c.append(zero, k, k, q=k, q_out=out, rope=rope)
+        assert torch.equal(c.v_tail[0, 0, 0], one.view(64))
+    assert torch.equal(caches[0].k_tail, caches[1].k_tail)
