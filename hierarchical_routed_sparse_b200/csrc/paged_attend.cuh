@@ -45,8 +45,8 @@
 // they should be and weights down to 2^-24 of the largest keep all their bits,
 // whatever the values' sizes.  (Open rows take the largest of their values for
 // v, for W alone.)  log2 v counts as at least -90; values below 2^-90 lose
-// bits.  Parts of a head (warps, CTAs) leave the registers as finished
-// means with their R and sum, so W stays inside.
+// bits.  Parts of a head (warps, CTAs) are joined as means by their shares of
+// the common sum, so W stays a warp's own.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -248,8 +248,8 @@ template <int D> struct Running {
         l1 = p[96];
         down = __float_as_uint(p[128]);
     }
-    // Means o [G][D] (zeros where no key was met), r [G], l [G] of this warp.
-    __device__ __forceinline__ void store(float* o, float* r, float* l, int G, int lane)
+    // o [G][D], r [G], l [G] of this warp, and f [G] that make means of o.
+    __device__ __forceinline__ void store(float* o, float* r, float* l, float* f, int G, int lane)
     {
         const int g = lane >> 2, t = lane & 3;
 #pragma unroll
@@ -260,15 +260,15 @@ template <int D> struct Running {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             if (2 * t + e >= G) continue;
-            const float l_ = e ? l1 : l0, inv = l_ == 0.f ? 0.f : rcp(l_);
-            const float up = __uint_as_float(0x7F000000u - __float_as_uint(e ? down1() : down0()));
             float* row = o + (2 * t + e) * D + (D / 8) * g;
 #pragma unroll
             for (int i = 0; i < kM; ++i)
-                *reinterpret_cast<float2*>(row + 2 * i) = make_float2(acc[i][e] * inv * up, acc[i][2 + e] * inv * up);
+                *reinterpret_cast<float2*>(row + 2 * i) = make_float2(acc[i][e], acc[i][2 + e]);
             if (g == 0) {
                 r[2 * t + e] = e ? R1 : R0;
-                l[2 * t + e] = l_;
+                const float sum = e ? l1 : l0;       // at least 1 where a key was met
+                l[2 * t + e] = sum;
+                f[2 * t + e] = sum == 0.f ? 0.f : __uint_as_float(0x7F000000u - __float_as_uint(e ? down1() : down0())) * rcp(sum);
             }
         }
     }

@@ -388,8 +388,8 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 4 ? 4 : 2) paged_decode
     float* om = reinterpret_cast<float*>(sm + L.merge);          // [kWarps][G][D]
     float* rm = om + kWarps * G * D;                             // [kWarps][G] references
     float* lm = rm + kWarps * G;                                 // [kWarps][G] sums
-    float* fm = lm + kWarps * G;                                 // [kWarps][G] shares
-    run.store(om + warp * G * D, rm + warp * G, lm + warp * G, G, lane);
+    float* fm = lm + kWarps * G;                                 // [kWarps][G] factors: of a mean, then times its share
+    run.store(om + warp * G * D, rm + warp * G, lm + warp * G, fm + warp * G, G, lane);
     __syncthreads();
     const int part = D / S, lg = __ffs(part) - 1;    // elements of a head's output that a CTA combines
     float* inbox = reinterpret_cast<float*>(sm + L.inbox);       // [S][G][part], then [S][G] references, sums, shares
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 4 ? 4 : 2) paged_decode
         const bool is = hd < G && w < kWarps;
         float M = is ? rm[w * G + hd] : kFloor, l = is ? lm[w * G + hd] : 0.f;
         const float f = join_parts<8>(M, l, S == 1);
-        if (is) fm[w * G + hd] = f;
+        if (is) fm[w * G + hd] *= f;
         if (S > 1) {
             if (hd < G && w < S) {
                 sm100::st_cluster_f32(peer_addr(smem_u32(ibr + rank * G + hd), w), M);

@@ -199,13 +199,13 @@ __global__ void __launch_bounds__(kThreads, kPerSm) paged_dense_kernel(const __g
         }
         held.attend(run, q, G, g.s.scale * kLog2e);
 
-        // The warps' parts meet; f: a warp's share of the sum.
+        // The warps' parts meet, each times its factor for a mean and its share of the sum.
         __syncthreads();
         float* om = reinterpret_cast<float*>(sm);    // [kWarps][G][D]
-        float* rm = om + kWarps * G * D;             // [kWarps][G] references, then sums, then shares
+        float* rm = om + kWarps * G * D;             // [kWarps][G] references, then sums, then factors
         float* lm = rm + kWarps * G;
         float* fm = lm + kWarps * G;
-        run.store(om + warp * G * D, rm + warp * G, lm + warp * G, G, lane);
+        run.store(om + warp * G * D, rm + warp * G, lm + warp * G, fm + warp * G, G, lane);
         __syncthreads();
         const bool whole = from == 0 && to == n;
         float* part = g.parts + (2 * (int64_t)blockIdx.x + (from == 0)) * part_floats(g.s);
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) paged_dense_kernel(const __g
             const bool is = hd < G && w < kWarps;
             float M = is ? rm[w * G + hd] : kFloor, l = is ? lm[w * G + hd] : 0.f;
             const float f = join_parts<8>(M, l, whole);
-            if (is) fm[w * G + hd] = f;
+            if (is) fm[w * G + hd] *= f;
             if (is && w == 0) {
                 if (whole) {
                     g.lse[head0 + hd] = (M + log2f(l)) * kLn2;
