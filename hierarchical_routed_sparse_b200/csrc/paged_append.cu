@@ -17,9 +17,14 @@
 // group's maximum is one warp reduction and nothing passes through shared
 // memory but the chunk summary) or some q-heads of it.  The kernel is bound
 // by the bytes of q, k, v and what it writes for prompts (16384 tokens, 32
-// q-heads, 8 kv-heads, d 128: 387 MB in 62 us, 6.2 TB/s), and by a launch
-// and three dependent loads for single tokens (2 us for one sequence, 7 us
-// for 64 of which eight complete a chunk).
+// q-heads, 8 kv-heads, d 128: 387 MB in 62 us, 6.2 TB/s, in a captured graph, 67
+// us, 5.8 TB/s, called on ever new tokens), and by a launch and three
+// dependent loads for single tokens (2 us for one sequence, 7 us for 64 of
+// which eight complete a chunk, in a captured graph; a call from Python takes
+// the host 9.5 us).  For 64 single tokens the grid is 576 CTAs on the 444 places
+// that three CTAs an SM leave, and 8 of a CTA's threads a row at work where no
+// chunk closes; for ragged prompts one CTA does two chunks in a row wherever a
+// call closes one and opens the next.
 //
 // Positions are moved by a call of their own, behind the rule that the append
 // itself goes by (sequence()): by what it took, so that an empty slot stays

@@ -5,9 +5,10 @@
 // in the open rows already).  With u = the sum of the kv-head's q-heads'
 // queries, chunk c < p / 64 scores u . csum[c]; the k_c highest are kept, then
 // the k_g highest of their groups by u . gsum.  Scores are formed in float64:
-// products of float32 values are exact there and a sum of 128 of them keeps
-// 2^-46, so which of two near candidates is kept is what the definition says
-// and not what an order of summation makes of it.  Every q-head attends the
+// a score is off by at most (d + 8) 2^-53 sum |u_i| |csum_i| (u is a rounded
+// sum of up to eight queries, so not every product is exact), and only
+// candidates that lie closer than that can change places with the order of
+// summation, which is fixed.  Every q-head attends the
 // kept groups' held values and the open rows 0 .. p % 64:
 //     O = softmax(scale q K^T) V,  lse = log sum exp (scale q K^T).
 //
@@ -23,10 +24,14 @@
 //     every head's output (distributed shared memory).
 //
 // A step is a chain of about ten dependent steps (position, scores, exchange,
-// selection, group scores, exchange, selection, tiles, merge, exchange) of
-// 0.5 - 2 us each, which bounds it: 13.5 us for one sequence at 16K context
-// (8 kv-heads, d 128, k_c 8, k_g 32; 2.3 MB), 37.4 us for 64 (103 MB, 2.8 TB/s:
-// all score at once, then all wait for each other's loads in short chains).
+// selection, group scores, exchange, selection, tiles, merge, exchange),
+// which bounds it: 13.6 us for one sequence at 16K context (8 kv-heads, d 128,
+// k_c 8, k_g 32; 2.3 MB), 38.1 us for 64 (103 MB, 2.7 TB/s: all score at once,
+// then all wait for each other's loads in short chains).
+//
+// Registers: 128 a thread with 4 or 8 warps (four and two CTAs an SM), 168 with
+// 6.  At d = 128 the attention's loop wants more, and 80 - 250 bytes a thread
+// go to local memory there, 24 - 44 with 6 warps; at d = 64 at most 20.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -444,8 +449,9 @@ __global__ void __launch_bounds__(32 * kWarps, kWarps == 4 ? 4 : 2) paged_decode
     }
 }
 
-// CTAs per (batch, kv-head), a power of two, and warps of one.  Measured, k_c 8,
-// k_g 32, d 128, us a call ("4 x 6": four CTAs of 6 warps):
+// CTAs per (batch, kv-head), a power of two, and warps of one.  Measured when
+// the rule was made, k_c 8, k_g 32, d 128, bf16, us a call ("4 x 6": four CTAs of
+// 6 warps):
 //   16K, units    8: 1 x 8 15.7, 8 x 6 14.1, 8 x 8 14.5
 //                32: 1 x 8 16.0, 2 x 6 16.0, 4 x 6 14.2, 8 x 6 15.1
 //                64: 1 x 4 20.8, 1 x 8 16.1, 2 x 6 16.1, 4 x 6 15.9

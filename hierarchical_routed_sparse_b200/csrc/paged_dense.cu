@@ -12,9 +12,12 @@
 // the positions, which both kernels read on the device.
 //
 // The kernel streams every code once; what bounds it is instruction issue, at
-// about 800 a tile (paged_attend.cuh): 8 sequences of up to 16K, 8 kv-heads
-// (156 MB) take 37.9 us with the join, 4.1 TB/s, and one of 50000 with 2
-// kv-heads (26 MB) 13.8 us, most of it the two kernels' chains.
+// about 800 a tile (paged_attend.cuh; 930 with a warp's fixed part), 0.53 of a
+// scheduler's slots with 12 warps an SM: 8 sequences of up to 16K, 8 kv-heads
+// (156 MB) take 38 us with the join, 4.1 TB/s, and one of 50000 with 2
+// kv-heads (26 MB) 14 us, most of it the two kernels' chains.  At d = 128 up to
+// 120 bytes a thread of the float32 kernel's 168 registers' worth go to local
+// memory, 24 of the bf16 one's.
 #include "paged.cuh"
 #include "paged_attend.cuh"
 #include "sm100.cuh"

@@ -423,8 +423,10 @@ typedef struct hga_paged_cache {
  * rows of one head; a = max |x|, L = 127 or 448) is held as
  *     scale = a' / L, code = round(x * (L * (1 / a'))), a' = max(a, L 2^-126)
  * (to nearest even); a group with a value that is not finite gets a NaN
- * scale.  Appending tokens one by one, or all at once, leaves the same cache
- * bit for bit. */
+ * scale.  Summaries are finite wherever the keys are.  Appending tokens one
+ * by one, or all at once, leaves the same pages and the same open rows
+ * 0 .. (last position) % 64 bit for bit (behind them may be rows of an earlier
+ * chunk). */
 int hga_paged_append(const hga_paged_params* p, const hga_paged_cache* c, const int32_t* pos,
                      const int32_t* cu_tokens, int64_t N, const void* q, int64_t q_token, int64_t q_head,
                      const void* k, int64_t k_token, int64_t k_head, const void* v, int64_t v_token,
@@ -456,9 +458,11 @@ size_t hga_paged_workspace_size(const hga_paged_params* p);
  * sequence, O = 0, lse = -inf, index rows -1).  As hga_decode: chunks
  * c < pos / 64 are routed on csum with the sum of the kv-head's G queries
  * (top k_c), then their groups on gsum (top k_g; equal scores go to the lower
- * index), with scores formed in float64; each q-head attends the routed
+ * index, a NaN is above all others), with scores formed in float64; each q-head attends the routed
  * groups' held values and the open rows 0 .. pos % 64.  k_c = k_g = HGA_ALL
- * is attention over the whole cache.
+ * is attention over the whole cache.  Held and open rows may be any finite
+ * floats, as long as the scores are; values below 2^-90 and queries below
+ * 2^-120 lose bits.
  *   q     [B][Hq][d] (dtype, dense; rotated)
  *   O     [B][Hq][d] float32;  lse [B][Hq] float32, natural log
  *   cidx  [B][Hkv][wc], gidx [B][Hkv][wg] int32 (hga_paged_widths), written;
