@@ -48,3 +48,18 @@ def test_a_bad_page_is_reported(k_c, k_g):
     c.table[0, 1] = 1
     c.decode(_int32([149]), q, O, lse, *rows)
     assert torch.isfinite(O).all() and hga.device_check() == 0
+
+
+def test_a_step_past_the_end_is_reported_and_not_counted():
+    st = hga.PagedDecodeState(2, 4, 2, 64, 64, 1, 4, rope=hga.rope_table(64, 64))
+    x = torch.randn(2, 8, 64, device="cuda").bfloat16()
+    st.pos.copy_(_int32([63, 5]))
+    st.step(x[:, :4], x[:, 4:6], x[:, 6:])
+    assert st.pos.tolist() == [64, 6]
+    with pytest.raises(hga.HGAError) as e:
+        st.step(x[:, :4], x[:, 4:6], x[:, 6:])
+    assert e.value.code == hga.HGA_ERR_DEVICE_CHECK and st.pos.tolist() == [64, 6]
+    with pytest.raises(hga.HGAError) as e:
+        st.cache.advance(st.pos)
+    assert e.value.code == hga.HGA_ERR_DEVICE_CHECK
+    assert st.pos.tolist() == [64, 7] and hga.device_check() == 0
